@@ -24,6 +24,9 @@ DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3}
 MOE_LAYOUT_KN, MOE_LAYOUT_NK = range(2)
 LAYOUTS = {"kn": MOE_LAYOUT_KN, "nk": MOE_LAYOUT_NK}
 
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = range(2)
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
 EXPORTS = (
     "moe_status_string", "moe_check_problem", "moe_workspace_size",
     "moe_dispatch_workspace_size",
@@ -34,6 +37,10 @@ EXPORTS = (
     "moe_quantize_fp8_blocks",
     "moe_eplb_hottest_map", "moe_eplb_plan", "moe_eplb_rank_map",
     "moe_eplb_record_load",
+    "moe_check_router", "moe_route_scored_workspace_size", "moe_route_scored",
+    "moe_route_scored_backward", "moe_check_norm", "moe_residual_norm",
+    "moe_residual_norm_workspace_size", "moe_residual_norm_backward",
+    "moe_combine_norm", "moe_combine_backward", "moe_layer_forward_scored",
 )
 MOE_STAGE_EVENTS = 8
 STAGES = ("route", "dispatch_index", "gather", "tiles", "gate_up", "down",
@@ -59,6 +66,23 @@ class Weights(ctypes.Structure):
         "sh_up", "sh_down", "sh_s_gate", "sh_s_up", "sh_s_down")]
 
 
+class Router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "T", "E", "k", "score", "groups", "topk_groups", "group_top",
+        "renormalize", "logits_dtype")] + [
+        ("scale", ctypes.c_float), ("logits_stride", ctypes.c_int64)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "T", "H", "block_dtype", "resid_dtype", "out_dtype", "gain_dtype")] + [
+        (n, ctypes.c_float) for n in ("eps", "gain_offset",
+                                      "residual_scale")] + [
+        (n, ctypes.c_int32) for n in ("gate_rows", "gate_cols")] + [
+        (n, ctypes.c_int64) for n in ("block_stride", "resid_stride",
+                                      "resid_out_stride", "out_stride")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -81,6 +105,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, V, S, I32 = (ctypes.POINTER(Problem), ctypes.c_void_p,
                         ctypes.c_size_t, ctypes.c_int32)
+        R, N = ctypes.POINTER(Router), ctypes.POINTER(Norm)
         sig = {
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "moe_check_problem": (ctypes.c_int, [P]),
@@ -116,6 +141,22 @@ def lib() -> ctypes.CDLL:
                                                  I32, V, V, V]),
             "moe_eplb_record_load": (ctypes.c_int, [V, I32, I32,
                                                     ctypes.c_int64, V, V, V]),
+            "moe_check_router": (ctypes.c_int, [R]),
+            "moe_route_scored_workspace_size": (ctypes.c_int, [
+                R, ctypes.POINTER(S)]),
+            "moe_route_scored": (ctypes.c_int, [R, V, V, V, V, V, V, S, V]),
+            "moe_route_scored_backward": (ctypes.c_int, [R, V, V, V, V, V]),
+            "moe_check_norm": (ctypes.c_int, [N]),
+            "moe_residual_norm": (ctypes.c_int, [N] + [V] * 8),
+            "moe_residual_norm_workspace_size": (ctypes.c_int, [
+                N, ctypes.POINTER(S)]),
+            "moe_residual_norm_backward": (ctypes.c_int, [N] + [V] * 13 +
+                                           [S, V]),
+            "moe_combine_norm": (ctypes.c_int, [P, N] + [V] * 12),
+            "moe_combine_backward": (ctypes.c_int, [P] + [V] * 8),
+            "moe_layer_forward_scored": (ctypes.c_int, [
+                P, R, N, V, V, V, ctypes.POINTER(Weights)] + [V] * 11 +
+                [S, V]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -381,6 +422,132 @@ def moe_eplb_record_load(expert_counts, E: int, window: int, step: int,
                                       current_stream() if stream is None
                                       else stream),
            "moe_eplb_record_load")
+
+
+# ------------------------------ scored routing, residual norm, gradients
+def make_router(T, E, k, score="softmax", groups=1, topk_groups=1,
+                group_top=1, renormalize=True, scale=1.0, logits="f32",
+                logits_stride=None) -> Router:
+    return Router(T, E, k, SCORES[score], groups, topk_groups, group_top,
+                  int(bool(renormalize)), DTYPES[logits], scale,
+                  E if logits_stride is None else logits_stride)
+
+
+def make_norm(T, H, block="bf16", resid="bf16", out="bf16", gain="f32",
+              eps=1e-6, gain_offset=0.0, residual_scale=1.0, gate_shape=None,
+              block_stride=None, resid_stride=None, resid_out_stride=None,
+              out_stride=None) -> Norm:
+    """``gate_shape``: (1 or T, 1 or H), None without a gate; strides default
+    to H."""
+    rows, cols = (1, 1) if gate_shape is None else gate_shape
+    strides = [H if v is None else v for v in (
+        block_stride, resid_stride, resid_out_stride, out_stride)]
+    return Norm(T, H, DTYPES[block], DTYPES[resid], DTYPES[out], DTYPES[gain],
+                eps, gain_offset, residual_scale, rows, cols, *strides)
+
+
+def _enqueue(name, first, stream, check, *args) -> int:
+    """Call an entry point on ``stream``, or on the current stream of the
+    device that holds ``first`` (with that device current)."""
+    fn = getattr(lib(), name)
+    if stream is not None:
+        st = fn(*args, stream)
+    else:
+        dev = getattr(first, "device", None)
+        if dev is not None and dev.type == "cuda":
+            import torch
+            if dev.index != torch.cuda.current_device():
+                with torch.cuda.device(dev):
+                    st = fn(*args, current_stream())
+            else:
+                st = fn(*args, current_stream())
+        else:
+            st = fn(*args, current_stream())
+    if check:
+        _check(st, name)
+    return st
+
+
+def moe_check_router(r: Router) -> int:
+    return lib().moe_check_router(ctypes.byref(r))
+
+
+def moe_check_norm(n: Norm) -> int:
+    return lib().moe_check_norm(ctypes.byref(n))
+
+
+def moe_route_scored_workspace_size(r: Router) -> int:
+    return _ws(lib().moe_route_scored_workspace_size, r)
+
+
+def moe_residual_norm_workspace_size(n: Norm) -> int:
+    return _ws(lib().moe_residual_norm_workspace_size, n)
+
+
+def moe_route_scored(r: Router, logits, bias, topk_ids, topk_w,
+                     expert_counts=None, workspace=None, ws_bytes=0,
+                     stream=None, check=True) -> int:
+    return _enqueue("moe_route_scored", logits, stream, check,
+                    ctypes.byref(r), ptr(logits), ptr(bias), ptr(topk_ids),
+                    ptr(topk_w), ptr(expert_counts), ptr(workspace), ws_bytes)
+
+
+def moe_route_scored_backward(r: Router, logits, topk_ids, d_topk_w, d_logits,
+                              stream=None, check=True) -> int:
+    return _enqueue("moe_route_scored_backward", logits, stream, check,
+                    ctypes.byref(r), ptr(logits), ptr(topk_ids),
+                    ptr(d_topk_w), ptr(d_logits))
+
+
+def moe_residual_norm(n: Norm, y, resid, post_gain, gate, pre_gain, resid_out,
+                      x_out, stream=None, check=True) -> int:
+    return _enqueue("moe_residual_norm", resid, stream, check,
+                    ctypes.byref(n), ptr(y), ptr(resid), ptr(post_gain),
+                    ptr(gate), ptr(pre_gain), ptr(resid_out), ptr(x_out))
+
+
+def moe_residual_norm_backward(n: Norm, y, resid_out, post_gain, gate,
+                               pre_gain, d_x, d_resid_out, d_y, d_resid,
+                               d_post_gain, d_gate, d_pre_gain, workspace,
+                               ws_bytes, stream=None, check=True) -> int:
+    return _enqueue("moe_residual_norm_backward", workspace, stream, check,
+                    ctypes.byref(n), ptr(y), ptr(resid_out), ptr(post_gain),
+                    ptr(gate), ptr(pre_gain), ptr(d_x), ptr(d_resid_out),
+                    ptr(d_y), ptr(d_resid), ptr(d_post_gain), ptr(d_gate),
+                    ptr(d_pre_gain), ptr(workspace), ws_bytes)
+
+
+def moe_combine_norm(p: Problem, n: Norm, y_perm, pair_row, topk_w, y_shared,
+                     resid, post_gain, gate, pre_gain, block_out, resid_out,
+                     x_out, stream=None, check=True) -> int:
+    return _enqueue("moe_combine_norm", y_perm, stream, check,
+                    ctypes.byref(p), ctypes.byref(n), ptr(y_perm),
+                    ptr(pair_row), ptr(topk_w), ptr(y_shared), ptr(resid),
+                    ptr(post_gain), ptr(gate), ptr(pre_gain), ptr(block_out),
+                    ptr(resid_out), ptr(x_out))
+
+
+def moe_combine_backward(p: Problem, d_out, y_perm, pair_row, topk_w,
+                         d_y_perm, d_topk_w, d_y_shared, stream=None,
+                         check=True) -> int:
+    return _enqueue("moe_combine_backward", d_out, stream, check,
+                    ctypes.byref(p), ptr(d_out), ptr(y_perm), ptr(pair_row),
+                    ptr(topk_w), ptr(d_y_perm), ptr(d_topk_w),
+                    ptr(d_y_shared))
+
+
+def moe_layer_forward_scored(p: Problem, r: Router, n: Optional[Norm], logits,
+                             bias, x, weights: Weights, l2p, replica_count,
+                             resid, post_gain, gate, pre_gain, out, resid_out,
+                             x_out, expert_counts, workspace, ws_bytes,
+                             stream=None, check=True) -> int:
+    return _enqueue("moe_layer_forward_scored", x, stream, check,
+                    ctypes.byref(p), ctypes.byref(r),
+                    None if n is None else ctypes.byref(n), ptr(logits),
+                    ptr(bias), ptr(x), ctypes.byref(weights), ptr(l2p),
+                    ptr(replica_count), ptr(resid), ptr(post_gain), ptr(gate),
+                    ptr(pre_gain), ptr(out), ptr(resid_out), ptr(x_out),
+                    ptr(expert_counts), ptr(workspace), ws_bytes)
 
 
 # ------------------------------------------------- device weight plumbing

@@ -1,9 +1,11 @@
 // C ABI of the MoE layer: argument validation, workspace layout and the
 // launch sequence of each step.  No allocation, no synchronisation.
 #include <algorithm>
+#include <cmath>
 #include <numeric>
 #include <vector>
 
+#include "block.h"
 #include "common.h"
 
 using namespace moe;
@@ -451,14 +453,23 @@ moe_status moe_combine(const moe_problem* p, const float* y_perm,
                                    p->H, p->k, p->out_dtype, out, S(stream)));
 }
 
-static moe_status layer_impl(const moe_problem* p, const float* logits,
+// What the scored layer has in place of the router and the combine.
+struct ScoredLayer {
+  const moe_router* r;
+  const moe_norm* n;      // or null: the combine ends the layer
+  NormArgs norm;
+};
+
+static moe_status layer_impl(const moe_problem* p, const void* logits,
                              const float* bias, const void* x,
                              const moe_weights* w, const int32_t* l2p,
                              const int32_t* replica_count, void* out,
                              int32_t* expert_counts, void* workspace,
-                             size_t ws_bytes, void* stream, hipEvent_t* ev) {
+                             size_t ws_bytes, void* stream, hipEvent_t* ev,
+                             const ScoredLayer* scored = nullptr) {
   moe_status st = moe_check_problem(p);
   if (st != MOE_OK) return st;
+  const moe_norm* n = scored ? scored->n : nullptr;
   if ((st = check_map(p, l2p, replica_count)) != MOE_OK) return st;
   if ((st = check_weights(p, w)) != MOE_OK) return st;
   hipStream_t s = S(stream);
@@ -467,8 +478,8 @@ static moe_status layer_impl(const moe_problem* p, const float* logits,
       return hip_status(launch_fill_i32(expert_counts, 0, (size_t)p->E, s));
     return MOE_OK;
   }
-  if (!logits || !x || !out) return MOE_ERR_INVALID_ARGUMENT;
-  if (!al16(x) || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!logits || !x || (!n && !out)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al16(x) || (!n && !al16(out))) return MOE_ERR_INVALID_ARGUMENT;
   size_t need;
   moe_layer_workspace_size(p, &need);
   if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
@@ -495,13 +506,17 @@ static moe_status layer_impl(const moe_problem* p, const float* logits,
   // FP8 recipe: the router and the activation quantiser share one launch
   // (the quantiser reads only x), so the router's latency hides under the
   // quantiser's stream; the route stage then holds both.
-  const bool fp8_q = p->weight_dtype == MOE_FP8_E4M3 && p->E <= 256;
+  const bool fp8_q =
+      !scored && p->weight_dtype == MOE_FP8_E4M3 && p->E <= 256;
+  const float* lf = (const float*)logits;
   const hipError_t re =
-      fp8_q ? launch_route_quant_fp8(logits, bias, p->T, p->E, p->k, L.ids,
-                                     L.tw, (const bf16_t*)x, p->H, L.d.xq,
-                                     L.d.xs, s)
-            : launch_route_topk(logits, bias, p->T, p->E, p->k, L.ids, L.tw,
-                                nullptr, s);
+      scored ? launch_route_scored(scored->r, logits, bias, L.ids, L.tw,
+                                   nullptr, nullptr, s)
+      : fp8_q ? launch_route_quant_fp8(lf, bias, p->T, p->E, p->k, L.ids,
+                                       L.tw, (const bf16_t*)x, p->H, L.d.xq,
+                                       L.d.xs, s)
+              : launch_route_topk(lf, bias, p->T, p->E, p->k, L.ids, L.tw,
+                                  nullptr, s);
   if (re != hipSuccess) return MOE_ERR_HIP;
   if (ev) hipEventRecord(ev[1], s);
   st = dispatch_impl(p, x, L.ids, L.tw, l2p, replica_count, L.x_perm,
@@ -521,9 +536,15 @@ static moe_status layer_impl(const moe_problem* p, const float* logits,
                          L.y_shared, L.f, s, ev ? ev + 4 : nullptr,
                          L.row_token, /*tiles_ready=*/true);
   if (st != MOE_OK) return st;
-  st = hip_status(launch_combine(L.y_perm, L.pair_row, L.tw,
-                                 p->has_shared ? L.y_shared : nullptr, p->T,
-                                 p->H, p->k, p->out_dtype, out, s));
+  const float* ysh = p->has_shared ? L.y_shared : nullptr;
+  if (n) {
+    const CombineSource c{L.y_perm, L.pair_row, L.tw, ysh, p->k,
+                          (int)cap_rows(p), out};
+    st = hip_status(launch_residual_norm(n, scored->norm, &c, s));
+  } else {
+    st = hip_status(launch_combine(L.y_perm, L.pair_row, L.tw, ysh, p->T,
+                                   p->H, p->k, p->out_dtype, out, s));
+  }
   if (ev) hipEventRecord(ev[7], s);
   return st;
 }
@@ -553,6 +574,222 @@ moe_status moe_layer_forward_timed(const moe_problem* p, const float* logits,
   }
   return layer_impl(p, logits, bias, x, w, l2p, replica_count, out,
                     expert_counts, workspace, ws_bytes, stream, ev);
+}
+
+// ------------------------------------------------------- scored routing
+moe_status moe_check_router(const moe_router* r) {
+  if (!r) return MOE_ERR_INVALID_ARGUMENT;
+  if (r->T < 0 || r->E < 1 || r->k < 1 || r->k > r->E)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (r->groups < 1 || r->E % r->groups || r->topk_groups < 1 ||
+      r->topk_groups > r->groups || (r->group_top != 1 && r->group_top != 2))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((long)r->topk_groups * (r->E / r->groups) < r->k)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (r->renormalize != 0 && r->renormalize != 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(r->scale) || r->logits_stride < r->E)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (r->logits_dtype < MOE_F32 || r->logits_dtype > MOE_FP8_E4M3)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (r->logits_dtype == MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (r->k > MOE_KMAX || r->E > MOE_EMAX || r->groups > 64)
+    return MOE_ERR_UNSUPPORTED;
+  if ((double)r->T * r->k >= 2147483647.0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_route_scored_workspace_size(const moe_router* r, size_t* bytes) {
+  const moe_status st = moe_check_router(r);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+  *bytes = route_scored_partials(r) * sizeof(int32_t);
+  return MOE_OK;
+}
+
+moe_status moe_route_scored(const moe_router* r, const void* logits,
+                            const float* bias, int32_t* topk_ids,
+                            float* topk_w, int32_t* expert_counts,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  const moe_status st = moe_check_router(r);
+  if (st != MOE_OK) return st;
+  if (r->T == 0) {
+    if (expert_counts)
+      return hip_status(launch_fill_i32(expert_counts, 0, (size_t)r->E, S(stream)));
+    return MOE_OK;
+  }
+  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t need = route_scored_partials(r) * sizeof(int32_t);
+  if (expert_counts && need && (!workspace || ws_bytes < need))
+    return MOE_ERR_WORKSPACE;
+  return hip_status(launch_route_scored(r, logits, bias, topk_ids, topk_w,
+                                        expert_counts, (int32_t*)workspace,
+                                        S(stream)));
+}
+
+moe_status moe_route_scored_backward(const moe_router* r, const void* logits,
+                                     const int32_t* topk_ids,
+                                     const float* d_topk_w, void* d_logits,
+                                     void* stream) {
+  const moe_status st = moe_check_router(r);
+  if (st != MOE_OK) return st;
+  if (r->T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !d_topk_w || !d_logits || d_logits == logits)
+    return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(launch_route_scored_backward(r, logits, topk_ids, d_topk_w,
+                                                 d_logits, S(stream)));
+}
+
+// -------------------------------------------------------- residual norm
+moe_status moe_check_norm(const moe_norm* n) {
+  if (!n) return MOE_ERR_INVALID_ARGUMENT;
+  if (n->T < 0 || n->H < 1) return MOE_ERR_INVALID_ARGUMENT;
+  for (int d : {n->block_dtype, n->resid_dtype, n->out_dtype, n->gain_dtype})
+    if (d < MOE_F32 || d > MOE_FP8_E4M3) return MOE_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(n->eps) || n->eps < 0.0f ||
+      !std::isfinite(n->gain_offset) || !std::isfinite(n->residual_scale))
+    return MOE_ERR_INVALID_ARGUMENT;
+  for (int64_t s : {n->block_stride, n->resid_stride, n->resid_out_stride,
+                    n->out_stride})
+    if (s < n->H) return MOE_ERR_INVALID_ARGUMENT;
+  for (int d : {n->block_dtype, n->resid_dtype, n->out_dtype, n->gain_dtype})
+    if (d == MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (n->H > 16384) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static bool gate_shape_ok(const moe_norm* n) {
+  return (n->gate_rows == 1 || n->gate_rows == n->T) &&
+         (n->gate_cols == 1 || n->gate_cols == n->H);
+}
+
+// the operands that a forward call needs besides its block
+static moe_status check_norm_forward(const moe_norm* n, const NormArgs& a) {
+  if (!a.resid || (!a.resid_out && !a.x_out)) return MOE_ERR_INVALID_ARGUMENT;
+  if ((a.pre_gain != nullptr) != (a.x_out != nullptr))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a.gate && !gate_shape_ok(n)) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+moe_status moe_residual_norm(const moe_norm* n, const void* y,
+                             const void* resid, const void* post_gain,
+                             const float* gate, const void* pre_gain,
+                             void* resid_out, void* x_out, void* stream) {
+  moe_status st = moe_check_norm(n);
+  if (st != MOE_OK) return st;
+  if (n->T == 0) return MOE_OK;
+  const NormArgs a{y, resid, post_gain, gate, pre_gain, resid_out, x_out};
+  if (!y && (post_gain || gate)) return MOE_ERR_INVALID_ARGUMENT;
+  if ((st = check_norm_forward(n, a)) != MOE_OK) return st;
+  return hip_status(launch_residual_norm(n, a, nullptr, S(stream)));
+}
+
+moe_status moe_residual_norm_workspace_size(const moe_norm* n, size_t* bytes) {
+  const moe_status st = moe_check_norm(n);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+  *bytes = norm_grad_partials(n) * sizeof(float);
+  return MOE_OK;
+}
+
+moe_status moe_residual_norm_backward(
+    const moe_norm* n, const void* y, const void* resid_out,
+    const void* post_gain, const float* gate, const void* pre_gain,
+    const void* d_x, const void* d_resid_out, void* d_y, void* d_resid,
+    float* d_post_gain, float* d_gate, float* d_pre_gain, void* workspace,
+    size_t ws_bytes, void* stream) {
+  const moe_status st = moe_check_norm(n);
+  if (st != MOE_OK) return st;
+  if ((d_post_gain && !post_gain) || (d_gate && !gate) ||
+      (d_pre_gain && !pre_gain))
+    return MOE_ERR_INVALID_ARGUMENT;
+  // (a batch of no rows may come without its row arrays)
+  if (n->T > 0) {
+    if (!y && (post_gain || gate)) return MOE_ERR_INVALID_ARGUMENT;
+    if ((pre_gain != nullptr) != (d_x != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+    if (pre_gain ? !resid_out : !d_resid_out) return MOE_ERR_INVALID_ARGUMENT;
+    if (!d_y && !d_resid && !d_post_gain && !d_gate && !d_pre_gain)
+      return MOE_ERR_INVALID_ARGUMENT;
+    const size_t need = norm_grad_partials(n) * sizeof(float);
+    if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  }
+  if (gate && !gate_shape_ok(n)) return MOE_ERR_INVALID_ARGUMENT;
+  const NormGradArgs a{y, resid_out, post_gain, gate, pre_gain, d_x,
+                       d_resid_out, d_y, d_resid, d_post_gain, d_gate,
+                       d_pre_gain};
+  return hip_status(launch_residual_norm_backward(n, a, (float*)workspace,
+                                                  S(stream)));
+}
+
+// ------------------------------------ the combine's end and its gradients
+static moe_status check_combine_norm(const moe_problem* p, const moe_norm* n,
+                                     const NormArgs& a) {
+  moe_status st = moe_check_norm(n);
+  if (st != MOE_OK) return st;
+  if (n->T != p->T || n->H != p->H) return MOE_ERR_INVALID_ARGUMENT;
+  return p->T == 0 ? MOE_OK : check_norm_forward(n, a);
+}
+
+moe_status moe_combine_norm(const moe_problem* p, const moe_norm* n,
+                            const float* y_perm, const int32_t* pair_row,
+                            const float* topk_w, const float* y_shared,
+                            const void* resid, const void* post_gain,
+                            const float* gate, const void* pre_gain,
+                            void* block_out, void* resid_out, void* x_out,
+                            void* stream) {
+  moe_status st = moe_check_problem(p);
+  if (st != MOE_OK) return st;
+  const NormArgs a{nullptr, resid, post_gain, gate, pre_gain, resid_out, x_out};
+  if ((st = check_combine_norm(p, n, a)) != MOE_OK) return st;
+  if (p->T == 0) return MOE_OK;
+  if (!y_perm || !pair_row || !topk_w) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al16(y_perm) || !al16(y_shared)) return MOE_ERR_INVALID_ARGUMENT;
+  const CombineSource c{y_perm, pair_row, topk_w, y_shared, p->k,
+                        (int)cap_rows(p), block_out};
+  return hip_status(launch_residual_norm(n, a, &c, S(stream)));
+}
+
+moe_status moe_combine_backward(const moe_problem* p, const void* d_out,
+                                const float* y_perm, const int32_t* pair_row,
+                                const float* topk_w, float* d_y_perm,
+                                float* d_topk_w, float* d_y_shared,
+                                void* stream) {
+  const moe_status st = moe_check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->T == 0) return MOE_OK;
+  if (!d_out || !pair_row || !topk_w || (d_topk_w && !y_perm) ||
+      (!d_y_perm && !d_topk_w && !d_y_shared))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!al16(d_out) || !al16(y_perm) || !al16(d_y_perm) || !al16(d_y_shared))
+    return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(launch_combine_backward(
+      d_out, p->out_dtype, y_perm, pair_row, topk_w, p->T, p->H, p->k,
+      (int)cap_rows(p), d_y_perm, d_topk_w, d_y_shared, S(stream)));
+}
+
+moe_status moe_layer_forward_scored(
+    const moe_problem* p, const moe_router* r, const moe_norm* n,
+    const void* logits, const float* bias, const void* x,
+    const moe_weights* w, const int32_t* l2p, const int32_t* replica_count,
+    const void* resid, const void* post_gain, const float* gate,
+    const void* pre_gain, void* out, void* resid_out, void* x_out,
+    int32_t* expert_counts, void* workspace, size_t ws_bytes, void* stream) {
+  moe_status st = moe_check_problem(p);
+  if (st != MOE_OK) return st;
+  if ((st = moe_check_router(r)) != MOE_OK) return st;
+  if (r->T != p->T || r->E != p->E || r->k != p->k)
+    return MOE_ERR_INVALID_ARGUMENT;
+  const ScoredLayer sl{r, n, {nullptr, resid, post_gain, gate, pre_gain,
+                              resid_out, x_out}};
+  if (n) {
+    if ((st = check_combine_norm(p, n, sl.norm)) != MOE_OK) return st;
+  } else if (resid || post_gain || gate || pre_gain || resid_out || x_out) {
+    return MOE_ERR_INVALID_ARGUMENT;
+  }
+  return layer_impl(p, logits, bias, x, w, l2p, replica_count, out,
+                    expert_counts, workspace, ws_bytes, stream, nullptr, &sl);
 }
 
 moe_status moe_prepack_weights(const void* src, int32_t K, int32_t N,

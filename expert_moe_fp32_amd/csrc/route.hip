@@ -9,6 +9,7 @@
 // single-workgroup histogram of the chosen ids with one LDS copy per
 // wavefront; it stores the counts, so no atomics reach global memory (on
 // skewed routing the hot experts' counters would serialise them).
+#include "block.h"
 #include "route_row.h"
 
 namespace moe {
@@ -109,6 +110,12 @@ __global__ __launch_bounds__(256) void k_route_topk(
   }
 }
 
+hipError_t launch_count_ids(const int32_t* ids, int n, int E, int32_t* counts,
+                            hipStream_t s) {
+  k_count_ids<<<1, 1024, 0, s>>>(ids, n, E, counts);
+  return hipGetLastError();
+}
+
 hipError_t launch_route_topk(const float* logits, const float* bias, int T,
                              int E, int k, int32_t* ids, float* w,
                              int32_t* counts, hipStream_t s) {
@@ -134,8 +141,7 @@ hipError_t launch_route_topk(const float* logits, const float* bias, int T,
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !counts) return e;
-  k_count_ids<<<1, 1024, 0, s>>>(ids, T * k, E, counts);
-  return hipGetLastError();
+  return launch_count_ids(ids, T * k, E, counts, s);
 }
 
 }  // namespace moe

@@ -189,6 +189,22 @@ class DeviceLayer:
             self.p, logits, bias, x, self.weights, self.l2p, self.rep, b.out,
             b.counts if counts else None, b.ws_layer, b.ws_layer.numel())
 
+    def forward_scored(self, b: LayerBuffers, router: L.Router, logits, bias,
+                       x, norm: Optional[L.Norm] = None, resid=None,
+                       post_gain=None, gate=None, pre_gain=None,
+                       resid_out=None, x_out=None, counts=True, out=True):
+        return L.moe_layer_forward_scored(
+            self.p, router, norm, logits, bias, x, self.weights, self.l2p,
+            self.rep, resid, post_gain, gate, pre_gain, b.out if out else None,
+            resid_out, x_out, b.counts if counts else None, b.ws_layer,
+            b.ws_layer.numel())
+
+    def route_scored(self, b: LayerBuffers, router: L.Router, logits, bias):
+        n = L.moe_route_scored_workspace_size(router)
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        return L.moe_route_scored(router, logits, bias, b.ids, b.w, b.counts,
+                                  ws, n)
+
     def route(self, b: LayerBuffers, logits, bias):
         return L.moe_route_topk(self.p, logits, bias, b.ids, b.w, b.counts)
 
@@ -207,3 +223,15 @@ class DeviceLayer:
     def combine(self, b: LayerBuffers):
         return L.moe_combine(self.p, b.y_perm, b.pair_row, b.w, b.y_shared,
                              b.out)
+
+    def combine_norm(self, b: LayerBuffers, norm: L.Norm, resid, post_gain,
+                     gate, pre_gain, resid_out, x_out, out=True):
+        return L.moe_combine_norm(self.p, norm, b.y_perm, b.pair_row, b.w,
+                                  b.y_shared, resid, post_gain, gate,
+                                  pre_gain, b.out if out else None, resid_out,
+                                  x_out)
+
+    def combine_backward(self, b: LayerBuffers, d_out, d_y_perm, d_w,
+                         d_y_shared=None):
+        return L.moe_combine_backward(self.p, d_out, b.y_perm, b.pair_row,
+                                      b.w, d_y_perm, d_w, d_y_shared)

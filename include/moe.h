@@ -260,6 +260,210 @@ MOE_API moe_status moe_layer_forward(const moe_problem* p, const float* logits,
                              int32_t* expert_counts, void* workspace,
                              size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------ scored routing
+ * The router of models that score experts with a sigmoid or a softmax, keep a
+ * balance bias out of the weights and choose inside groups of experts. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* One router call.  Sizes: 1 <= k <= 16, E <= 1024, groups <= 64. */
+typedef struct {
+  int32_t T;             /* tokens                                           */
+  int32_t E;             /* experts                                          */
+  int32_t k;             /* experts per token                                */
+  int32_t score;         /* moe_score                                        */
+  int32_t groups;        /* equal groups of neighbouring experts (divides E);
+                            1 = no groups                                    */
+  int32_t topk_groups;   /* groups kept, 1 <= topk_groups <= groups; they hold
+                            at least k experts                               */
+  int32_t group_top;     /* a group's score sums its best 1 or 2 choices     */
+  int32_t renormalize;   /* 1: the k weights are divided by their sum        */
+  int32_t logits_dtype;  /* MOE_F32 or MOE_BF16, of logits and d_logits      */
+  float scale;           /* factor of every weight (finite)                  */
+  int64_t logits_stride; /* elements between rows of logits and d_logits, at
+                            least E (a slice of a wider array)               */
+} moe_router;
+
+/* Validate a router description (host only). */
+MOE_API moe_status moe_check_router(const moe_router* r);
+
+/* Bytes of scratch moe_route_scored needs when it counts the experts (host
+ * only; 256-byte aligned device memory; 0 for small batches). */
+MOE_API moe_status moe_route_scored_workspace_size(const moe_router* r,
+                                                   size_t* bytes);
+
+/* Scored routing.
+ *   score   s_e = sigmoid(l_e), or softmax over all E of the row
+ *   choice  c_e = s_e + bias_e (bias NULL: s_e); the bias balances the load
+ *           and never reaches the weights
+ *   groups  a group's score is the sum of its best group_top choices; the
+ *           topk_groups best groups stay
+ *   ids     slot j holds the j-th largest choice among the groups that stay
+ *   weights w_j = scale * s_j, or scale * s_j / sum_i s_i over the k chosen
+ * Scores, choices and group scores are evaluated in 64 bits, and of equal
+ * ones the lower id (of a group or an expert) comes first.
+ * Masked experts: a logit of -inf or NaN, or a bias of -inf or NaN, masks an
+ * expert; its logit of -inf or NaN also makes its score 0.  Masked experts
+ * and groups without an unmasked one come after all others, lower ids first
+ * (so ids are always valid); a masked expert adds nothing to its group's
+ * score.  Weights whose k scores sum to 0 (a row masked throughout) are 0.
+ * Logits of +inf share a softmax row equally among them.
+ *   logits        [T][logits_stride], the first E columns read
+ *   bias          [E] float32 or NULL
+ *   topk_ids      [T][k] int32 out
+ *   topk_w        [T][k] float32 out
+ *   expert_counts [E] int32 out, or NULL: pairs per expert over all T
+ *   workspace     of moe_route_scored_workspace_size bytes; unused (may be
+ *                 NULL) without expert_counts
+ * T = 0 clears expert_counts.  Identical inputs give identical outputs. */
+MOE_API moe_status moe_route_scored(const moe_router* r, const void* logits,
+                                    const float* bias, int32_t* topk_ids,
+                                    float* topk_w, int32_t* expert_counts,
+                                    void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/* Gradient of the weights of moe_route_scored with respect to the logits (the
+ * choice itself has none):
+ *   renormalize: ds_j = scale / S (dw_j - sum_i dw_i s_i / S), S = sum_i s_i
+ *   otherwise    ds_j = scale dw_j
+ *   sigmoid: dl_e = ds_j s_j (1 - s_j) for the expert of slot j, else 0
+ *   softmax: dl_e = s_e (ds_j [e in slot j] - sum_i ds_i s_i)
+ * evaluated in 64 bits and rounded once.  Experts with a logit of -inf or NaN
+ * get 0, and so do rows whose S is 0 under renormalize.
+ *   topk_ids [T][k] as moe_route_scored gave them (an id outside [0, E) gets
+ *            no gradient)
+ *   d_topk_w [T][k] float32
+ *   d_logits [T][logits_stride] out: the first E columns are written, all of
+ *            them */
+MOE_API moe_status moe_route_scored_backward(const moe_router* r,
+                                             const void* logits,
+                                             const int32_t* topk_ids,
+                                             const float* d_topk_w,
+                                             void* d_logits, void* stream);
+
+/* ------------------------------------------------ residual norm
+ * The end of one block and the start of the next in one pass over a token's
+ * row: the norm after a block, its gate and residual scale, the residual add,
+ * and the norm before the next block.  unit(z) = z / sqrt(mean(z^2) + eps):
+ *   v         = unit(y) * (gain_offset + post_gain)     (y without post_gain)
+ *   resid_out = resid + residual_scale * gate * v       (gate 1 without gate)
+ *   x_out     = unit(resid_out) * (gain_offset + pre_gain)
+ * Everything in float32; x_out is computed from the unrounded resid_out.
+ * Row arrays may have any alignment of their element type and any row stride
+ * from H on; 16-byte aligned ones with H and strides that are multiples of 8
+ * are fastest. */
+typedef struct {
+  int32_t T;                /* rows (tokens)                                 */
+  int32_t H;                /* columns, 1 <= H <= 16384                      */
+  int32_t block_dtype;      /* MOE_F32 or MOE_BF16: y, d_y                   */
+  int32_t resid_dtype;      /* resid, resid_out and their gradients          */
+  int32_t out_dtype;        /* x_out, d_x                                    */
+  int32_t gain_dtype;       /* post_gain, pre_gain                           */
+  float eps;                /* >= 0                                          */
+  float gain_offset;        /* added to the stored gains (0, or 1 for gains
+                               stored as a difference from 1)                */
+  float residual_scale;
+  int32_t gate_rows;        /* gate is [gate_rows][gate_cols] float32,       */
+  int32_t gate_cols;        /*   contiguous: gate_rows 1 or T, gate_cols 1 or
+                               H (both ignored without a gate)               */
+  int64_t block_stride;     /* elements between rows of y and d_y            */
+  int64_t resid_stride;     /* of resid and d_resid                          */
+  int64_t resid_out_stride; /* of resid_out and d_resid_out                  */
+  int64_t out_stride;       /* of x_out and d_x                              */
+} moe_norm;
+
+/* Validate a residual-norm description (host only). */
+MOE_API moe_status moe_check_norm(const moe_norm* n);
+
+/*   y         [T][block_stride] the block's output; NULL: no block (the norm
+ *             before the first one), then post_gain and gate are NULL
+ *   resid     [T][resid_stride]
+ *   post_gain [H] or NULL;  gate see moe_norm, or NULL;
+ *   pre_gain  [H], or NULL together with x_out (no norm before a next block)
+ *   resid_out [T][resid_out_stride] out, or NULL; may be resid itself
+ *   x_out     [T][out_stride] out
+ * At least one output is given; outputs overlap no input otherwise. */
+MOE_API moe_status moe_residual_norm(const moe_norm* n, const void* y,
+                                     const void* resid, const void* post_gain,
+                                     const float* gate, const void* pre_gain,
+                                     void* resid_out, void* x_out,
+                                     void* stream);
+
+/* Bytes of scratch of moe_residual_norm_backward (host only; 256-byte aligned
+ * device memory, not initialised). */
+MOE_API moe_status moe_residual_norm_workspace_size(const moe_norm* n,
+                                                    size_t* bytes);
+
+/* Gradients of moe_residual_norm.  With g the whole gradient of resid_out
+ * (d_resid_out plus what x_out's norm passes back):
+ *   d_resid = g
+ *   d_v = residual_scale * gate * g, through the norm after the block to d_y
+ * and the gradients of the gains and the gate, summed over the rows (the gate
+ * over what it is broadcast along) in a fixed order.
+ *   y           as in the forward; may be NULL without post_gain and gate
+ *   resid_out   the forward's output (may be NULL without pre_gain)
+ *   d_x         [T][out_stride]; given exactly when pre_gain is
+ *   d_resid_out [T][resid_out_stride] or NULL (zero)
+ *   d_y         [T][block_stride] out, or NULL
+ *   d_resid     [T][resid_stride] out, or NULL; may be d_resid_out itself
+ *   d_post_gain, d_pre_gain [H] float32 out, or NULL
+ *   d_gate      float32 out in the gate's shape, or NULL
+ * An output whose operand is absent is NULL.  T = 0 clears the gains' and the
+ * gate's gradients. */
+MOE_API moe_status moe_residual_norm_backward(
+    const moe_norm* n, const void* y, const void* resid_out,
+    const void* post_gain, const float* gate, const void* pre_gain,
+    const void* d_x, const void* d_resid_out, void* d_y, void* d_resid,
+    float* d_post_gain, float* d_gate, float* d_pre_gain, void* workspace,
+    size_t ws_bytes, void* stream);
+
+/* moe_combine and moe_residual_norm in one pass: the combined row stays in
+ * float32 registers and takes the place of y.  n->T = p->T, n->H = p->H.
+ *   block_out [T][block_stride] out, or NULL: the combined row in block_dtype
+ *             (what the gradients take as y)
+ * Other arguments as in the two; resid_out or x_out must be given. */
+MOE_API moe_status moe_combine_norm(
+    const moe_problem* p, const moe_norm* n, const float* y_perm,
+    const int32_t* pair_row, const float* topk_w, const float* y_shared,
+    const void* resid, const void* post_gain, const float* gate,
+    const void* pre_gain, void* block_out, void* resid_out, void* x_out,
+    void* stream);
+
+/* Gradients of moe_combine:
+ *   d_y_perm[pair_row[t][j]] = topk_w[t][j] * d_out[t]
+ *   d_topk_w[t][j]           = sum_h d_out[t][h] y_perm[pair_row[t][j]][h]
+ *                              (0 for a non-local pair)
+ *   d_y_shared[t]            = d_out[t]
+ * in float32, each sum in a fixed order.
+ *   d_out      [T][H] of out_dtype
+ *   d_y_perm   [cap][H] float32 out (rows of no pair untouched), or NULL
+ *   d_topk_w   [T][k] float32 out, or NULL (y_perm may then be NULL)
+ *   d_y_shared [T][H] float32 out, or NULL
+ * Each row belongs to one pair, as moe_dispatch makes them. */
+MOE_API moe_status moe_combine_backward(const moe_problem* p,
+                                        const void* d_out,
+                                        const float* y_perm,
+                                        const int32_t* pair_row,
+                                        const float* topk_w, float* d_y_perm,
+                                        float* d_topk_w, float* d_y_shared,
+                                        void* stream);
+
+/* The whole layer with scored routing, and the residual norm as its end:
+ * moe_route_scored -> dispatch -> grouped FFN -> moe_combine_norm (or, with
+ * n = NULL, moe_combine into out).  r's T, E and k are p's.
+ *   logits, bias   as in moe_route_scored
+ *   n = NULL:  out [T][H] out_dtype; the norm's arrays are NULL
+ *   n given:   out NULL, or the combined rows as moe_combine_norm's
+ *              block_out; resid, post_gain, gate, pre_gain, resid_out and
+ *              x_out as there
+ *   workspace  as for moe_layer_forward (moe_layer_workspace_size) */
+MOE_API moe_status moe_layer_forward_scored(
+    const moe_problem* p, const moe_router* r, const moe_norm* n,
+    const void* logits, const float* bias, const void* x,
+    const moe_weights* w, const int32_t* l2p, const int32_t* replica_count,
+    const void* resid, const void* post_gain, const float* gate,
+    const void* pre_gain, void* out, void* resid_out, void* x_out,
+    int32_t* expert_counts, void* workspace, size_t ws_bytes, void* stream);
+
 /* Profiling variant of moe_layer_forward: the same work, plus hipEventRecord
  * on `stream` at the stage boundaries, so a caller can time each stage with
  * hipEventElapsedTime.  events: HOST array of MOE_STAGE_EVENTS hipEvent_t

@@ -1,0 +1,252 @@
+"""Scored routing, residual norm and combine gradients without a GPU: every
+bad argument is refused with the documented status before a device is
+touched, and empty batches succeed."""
+import pytest
+
+import expert_moe_fp32_amd as m
+from expert_moe_fp32_amd import _lib as L
+
+BAD, UNSUP, WS = (L.MOE_ERR_INVALID_ARGUMENT, L.MOE_ERR_UNSUPPORTED,
+                  L.MOE_ERR_WORKSPACE)
+P = 4096                      # an address that is never read
+
+
+def router(**kw):
+    base = dict(T=64, E=256, k=8, score="sigmoid", groups=8, topk_groups=4,
+                group_top=2)
+    base.update(kw)
+    field = {n: base.pop(n) for n in list(base) if n.startswith("_")}
+    r = m.make_router(**base)
+    for n, v in field.items():
+        setattr(r, n[1:], v)
+    return r
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), L.MOE_OK),
+    (dict(T=0), L.MOE_OK),
+    (dict(T=-1), BAD),
+    (dict(k=0), BAD),
+    (dict(k=17, groups=1, topk_groups=1), UNSUP),
+    (dict(E=4, k=5, groups=1, topk_groups=1), BAD),
+    (dict(E=2048), UNSUP),
+    (dict(groups=0), BAD),
+    (dict(groups=7), BAD),                       # does not divide E
+    (dict(groups=128, topk_groups=64), UNSUP),
+    (dict(topk_groups=0), BAD),
+    (dict(topk_groups=9), BAD),
+    (dict(E=16, groups=8, topk_groups=2), BAD),  # keeps 4 of 8 experts wanted
+    (dict(group_top=0), BAD),
+    (dict(group_top=3), BAD),
+    (dict(_renormalize=2), BAD),
+    (dict(_score=2), BAD),
+    (dict(scale=float("nan")), BAD),
+    (dict(scale=float("inf")), BAD),
+    (dict(logits="bf16"), L.MOE_OK),
+    (dict(logits="fp8"), UNSUP),
+    (dict(_logits_dtype=9), BAD),
+    (dict(logits_stride=255), BAD),
+    (dict(logits_stride=257), L.MOE_OK),
+    (dict(T=2 ** 28), UNSUP),                    # T * k past 32 bits
+])
+def test_router_validation(kw, status):
+    r = router(**kw)
+    assert m.moe_check_router(r) == status
+    if status != L.MOE_OK:
+        assert m.moe_route_scored(r, P, P, P, P, P, P, 1 << 30, stream=0,
+                                  check=False) == status
+        assert m.moe_route_scored_backward(r, P, P, P, 2 * P, stream=0,
+                                           check=False) == status
+        with pytest.raises(m.MoeError):
+            m.moe_route_scored_workspace_size(r)
+
+
+def test_router_arguments():
+    r = router()
+    for miss in range(4):
+        args = [P, P, P, P]                # logits, bias, ids, weights
+        args[miss] = None
+        if miss == 1:
+            continue                       # the bias is optional
+        assert m.moe_route_scored(r, *args, stream=0, check=False) == BAD
+    for miss in range(4):
+        args = [P, P, P, 2 * P]
+        args[miss] = None
+        assert m.moe_route_scored_backward(r, *args, stream=0,
+                                           check=False) == BAD
+    assert m.moe_route_scored_backward(r, P, P, P, P, stream=0,
+                                       check=False) == BAD    # in place
+    big = router(T=100000)
+    need = m.moe_route_scored_workspace_size(big)
+    assert need > 0
+    for ws, n in ((None, need), (P, need - 1)):
+        assert m.moe_route_scored(big, P, P, P, P, P, ws, n, stream=0,
+                                  check=False) == WS
+
+
+def norm(**kw):
+    base = dict(T=8, H=256)
+    base.update(kw)
+    return m.make_norm(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), L.MOE_OK),
+    (dict(T=0), L.MOE_OK),
+    (dict(T=-1), BAD),
+    (dict(H=0), BAD),
+    (dict(H=1), L.MOE_OK),
+    (dict(H=16384), L.MOE_OK),
+    (dict(H=16385), UNSUP),
+    (dict(eps=-1e-6), BAD),
+    (dict(eps=float("nan")), BAD),
+    (dict(eps=0.0), L.MOE_OK),
+    (dict(residual_scale=float("inf")), BAD),
+    (dict(gain_offset=float("nan")), BAD),
+    (dict(block="fp8"), UNSUP),
+    (dict(resid="fp8"), UNSUP),
+    (dict(out="fp8"), UNSUP),
+    (dict(gain="fp8"), UNSUP),
+    (dict(block_stride=255), BAD),
+    (dict(resid_stride=255), BAD),
+    (dict(resid_out_stride=255), BAD),
+    (dict(out_stride=255), BAD),
+    (dict(out_stride=300), L.MOE_OK),
+])
+def test_norm_validation(kw, status):
+    n = norm(**kw)
+    assert m.moe_check_norm(n) == status
+    if status != L.MOE_OK:
+        assert m.moe_residual_norm(n, P, P, None, None, P, P, P, stream=0,
+                                   check=False) == status
+        with pytest.raises(m.MoeError):
+            m.moe_residual_norm_workspace_size(n)
+
+
+def forward(n, y=P, resid=P, post=None, gate=None, pre=P, ro=2 * P, x=3 * P):
+    return m.moe_residual_norm(n, y, resid, post, gate, pre, ro, x, stream=0,
+                               check=False)
+
+
+def test_norm_arguments():
+    n = norm()
+    assert forward(n, resid=None) == BAD
+    assert forward(n, pre=None) == BAD               # x_out without a gain
+    assert forward(n, x=None) == BAD                 # a gain without x_out
+    assert forward(n, pre=None, x=None, ro=None) == BAD
+    assert forward(n, y=None, post=P) == BAD
+    assert forward(n, y=None, gate=P) == BAD
+    for shape in ((2, 1), (1, 2), (0, 1), (8, 255), (256, 8)):
+        assert forward(norm(gate_shape=shape), gate=P) == BAD
+
+
+def backward(n, y=P, ro=P, post=P, gate=None, pre=P, d_x=P, d_ro=P, d_y=P,
+             d_r=P, d_post=P, d_gate=None, d_pre=P, ws=P, size=1 << 30):
+    return m.moe_residual_norm_backward(
+        n, y, ro, post, gate, pre, d_x, d_ro, d_y, d_r, d_post, d_gate, d_pre,
+        ws, size, stream=0, check=False)
+
+
+def test_norm_backward_arguments():
+    n = norm()
+    need = m.moe_residual_norm_workspace_size(n)
+    assert backward(n, size=need - 1) == WS
+    assert backward(n, ws=None) == WS
+    assert backward(n, y=None) == BAD
+    assert backward(n, ro=None) == BAD
+    assert backward(n, d_x=None) == BAD
+    assert backward(n, pre=None, d_pre=None) == BAD          # d_x without it
+    assert backward(n, pre=None, d_x=None) == BAD            # d_pre without it
+    assert backward(n, post=None) == BAD                     # d_post without it
+    assert backward(n, d_gate=P) == BAD                      # no gate
+    assert backward(n, pre=None, d_x=None, d_pre=None, d_ro=None) == BAD
+    assert backward(n, d_y=None, d_r=None, d_post=None, d_pre=None) == BAD
+    assert backward(norm(gate_shape=(3, 1)), gate=P) == BAD
+
+
+def problem(**kw):
+    base = dict(T=8, H=256, I=128, E=16, k=4, num_local=8)
+    base.update(kw)
+    return m.make_problem(**base)
+
+
+def test_combine_norm_arguments():
+    p, n = problem(), norm()
+
+    def call(p=p, n=n, y=P, rows=P, w=P, sh=None, resid=P, pre=P, ro=P, x=P,
+             gate=None):
+        return m.moe_combine_norm(p, n, y, rows, w, sh, resid, None, gate,
+                                  pre, None, ro, x, stream=0, check=False)
+
+    assert call(y=None) == BAD
+    assert call(rows=None) == BAD
+    assert call(w=None) == BAD
+    assert call(resid=None) == BAD
+    assert call(x=None) == BAD
+    assert call(ro=None, x=None, pre=None) == BAD
+    assert call(y=P + 4) == BAD
+    assert call(sh=P + 8) == BAD
+    assert call(n=norm(T=9)) == BAD
+    assert call(n=norm(H=384)) == BAD
+    assert call(n=norm(gate_shape=(2, 2)), gate=P) == BAD
+    assert call(n=norm(eps=-1.0)) == BAD
+    assert call(p=problem(H=200)) == UNSUP
+    assert call(p=problem(T=0), n=norm(T=0), y=None) == L.MOE_OK
+
+
+def test_combine_backward_arguments():
+    p = problem()
+
+    def call(d=P, y=P, rows=P, w=P, dy=P, dw=P, ds=None, p=p):
+        return m.moe_combine_backward(p, d, y, rows, w, dy, dw, ds, stream=0,
+                                      check=False)
+
+    assert call(d=None) == BAD
+    assert call(rows=None) == BAD
+    assert call(w=None) == BAD
+    assert call(y=None) == BAD                   # d_topk_w needs the rows
+    assert call(dy=None, dw=None) == BAD
+    for name in ("d", "y", "dy", "ds"):
+        assert call(**{name: P + 8}) == BAD
+    assert call(p=problem(T=0), d=None) == L.MOE_OK
+
+
+def test_scored_layer_arguments():
+    p, n, r = problem(), norm(), m.make_router(8, 16, 4)
+    w = L.Weights()
+    w.w_gate = w.w_up = w.w_down = P
+
+    def call(p=p, r=r, n=n, logits=P, x=P, weights=w, resid=P, pre=P, out=None,
+             ro=P, xo=P, ws=P, size=1 << 40):
+        return m.moe_layer_forward_scored(
+            p, r, n, logits, None, x, weights, None, None, resid, None, None,
+            pre, out, ro, xo, None, ws, size, stream=0, check=False)
+
+    assert call(r=m.make_router(9, 16, 4)) == BAD
+    assert call(r=m.make_router(8, 32, 4)) == BAD
+    assert call(r=m.make_router(8, 16, 3)) == BAD
+    assert call(r=m.make_router(8, 16, 4, groups=3)) == BAD
+    assert call(n=norm(H=128)) == BAD
+    assert call(logits=None) == BAD
+    assert call(x=None) == BAD
+    assert call(x=P + 2) == BAD
+    assert call(resid=None) == BAD
+    assert call(pre=None) == BAD
+    assert call(weights=L.Weights()) == BAD
+    assert call(n=None, out=P) == BAD            # the norm's arrays without it
+    none = dict(n=None, resid=None, pre=None, ro=None, xo=None)
+    assert call(**none) == BAD                   # no out either
+    assert call(**none, out=P, ws=None) == WS
+    assert call(size=m.moe_layer_workspace_size(p) - 1) == WS
+
+
+def test_zero_tokens_enqueue_nothing():
+    r, n = router(T=0), norm(T=0)
+    assert m.moe_route_scored(r, None, None, None, None, stream=0,
+                              check=False) == L.MOE_OK
+    assert m.moe_route_scored_backward(r, None, None, None, None, stream=0,
+                                       check=False) == L.MOE_OK
+    assert m.moe_residual_norm(n, None, None, None, None, None, None, None,
+                               stream=0, check=False) == L.MOE_OK
+    assert m.moe_residual_norm_backward(
+        n, *[None] * 12, None, 0, stream=0, check=False) == L.MOE_OK
