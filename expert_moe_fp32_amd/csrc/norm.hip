@@ -1,135 +1,20 @@
-// Residual norm (moe_residual_norm), the combine fused into it
-// (moe_combine_norm), and its gradients.
+// Residual norm (moe_residual_norm) and the combine fused into it
+// (moe_combine_norm).
 //
-// One workgroup holds a token's row in registers, eight neighbouring columns
-// a thread and pass (VPT passes), so every array is read and written once and
-// the two mean squares cost one exchange of a partial sum per wavefront each.
-// Bound by HBM: forward 2 rows in, 2 rows out; backward 4 in, 2 out.
+// A workgroup holds a token's row in registers, so every array is read and
+// written once, and the two mean squares cost one exchange of a partial sum
+// per wavefront each.  The workgroups stay and walk the rows: gains are read
+// once, and a row's loads are in flight while the row before it is worked on.
+// Bound by HBM.
+#include <algorithm>
 #include <type_traits>
 
 #include "block.h"
+#include "rows.h"
 
 namespace moe {
 
 namespace {
-
-typedef __attribute__((ext_vector_type(8))) float f32x8_t;
-typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
-typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
-
-// ------------------------------------------------ eight columns of a row
-// AL: the eight columns are all there and 16-byte aligned.  Otherwise `n` of
-// them are there, at the alignment of the element type.
-template <typename T, bool AL>
-__device__ __forceinline__ f32x8_t load8(const T* p, int n) {
-  f32x8_t v;
-  if constexpr (sizeof(T) == 2) {
-    if (AL || n >= 8) {
-      const u32x4_t u = AL ? *(const u32x4_t*)p : (u32x4_t)*(const u32x4_any_t*)p;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_to_f32(p[i]) : 0.0f;
-    }
-  } else {
-    if (AL || n >= 8) {
-      f32x4_t a, b;
-      if (AL) {
-        a = *(const f32x4_t*)p;
-        b = *(const f32x4_t*)(p + 4);
-      } else {
-        a = *(const f32x4_any_t*)p;
-        b = *(const f32x4_any_t*)(p + 4);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
-    }
-  }
-  return v;
-}
-
-template <typename T, bool AL>
-__device__ __forceinline__ void store8(T* p, f32x8_t v, int n) {
-  if constexpr (sizeof(T) == 2) {
-    typedef __attribute__((ext_vector_type(8))) __bf16 b8;
-    const b8 b = __builtin_convertvector(v, b8);   // nearest even
-    const u32x4_t u = __builtin_bit_cast(u32x4_t, b);
-    if (AL) {
-      *(u32x4_t*)p = u;
-    } else if (n >= 8) {
-      *(u32x4_any_t*)p = u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (bf16_t)(u[i >> 1] >> (16 * (i & 1)));
-    }
-  } else {
-    const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-    if (AL) {
-      *(f32x4_t*)p = a;
-      *(f32x4_t*)(p + 4) = b;
-    } else if (n >= 8) {
-      *(f32x4_any_t*)p = a;
-      *(f32x4_any_t*)(p + 4) = b;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = v[i];
-    }
-  }
-}
-
-// a gain vector's eight values, whichever type it is stored in
-template <bool AL>
-__device__ __forceinline__ f32x8_t load_gain(const void* g, int bf16, int col,
-                                             int n, float offset) {
-  f32x8_t v = bf16 ? load8<bf16_t, AL>((const bf16_t*)g + col, n)
-                   : load8<float, AL>((const float*)g + col, n);
-  v += offset;
-  return v;
-}
-
-__device__ __forceinline__ float dot8(f32x8_t a, f32x8_t b) {
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s = __builtin_fmaf(a[i], b[i], s);
-  return s;
-}
-
-// sums of N values over the workgroup, the same in every thread; `buf` holds
-// 16 x N floats and is not used again before another barrier
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* buf) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int waves = blockDim.x >> 6;
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m, 64);
-  }
-  if (waves == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) buf[wv * N + i] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.0f;
-  for (int w = 0; w < waves; ++w) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += buf[w * N + i];
-  }
-}
 
 struct NormRun {
   moe_norm n;
@@ -137,328 +22,213 @@ struct NormRun {
   CombineSource c;
 };
 
-// ------------------------------------------------------------- forward
-template <typename YT, typename RT, typename XT, bool AL, int VPT, bool COMB>
-__global__ __launch_bounds__(1024) void k_residual_norm(NormRun q) {
+// KEEP: gains stay in registers and the next row is requested early.  Rows
+// too long for that (H > 8192) take 1024 threads, which have half the
+// registers, and do without both.
+constexpr int row_limit(int ept, bool keep) { return ept == 8 || !keep ? 1024 : 512; }
+
+// YT: the type of y (COMB: of the shared expert's row, float32), RT: of
+// resid; W columns a piece, EPT a thread
+template <typename YT, typename RT, int W, Fit FIT, int EPT, bool COMB,
+          bool STREAM, bool KEEP>
+__global__ __launch_bounds__(row_limit(EPT, KEEP)) void k_residual_norm(NormRun q) {
+  constexpr int P = EPT / W;
+  typedef Cols<W> V;
   __shared__ float red[2][2][16];      // [row parity][mean square][wavefront]
-  __shared__ int32_t s_row[2][MOE_KMAX];
-  __shared__ float s_w[2][MOE_KMAX];
-  __shared__ int s_n[2];
   const moe_norm& n = q.n;
-  const int H = n.H, NT = blockDim.x;
+  const int H = n.H, NT = blockDim.x, lane = threadIdx.x & 63;
+  const int waves = NT >> 6;
+  const long G = gridDim.x;
   const float inv_h = 1.0f / (float)H;
-  int par = 0;
-  for (long t = blockIdx.x; t < n.T; t += gridDim.x, par ^= 1) {
-    const RT* rr = (const RT*)q.a.resid + t * n.resid_stride;
-    f32x8_t y[VPT], r[VPT];
+  V post[KEEP ? P : 1], pre[KEEP ? P : 1];
+  Piece pc[P];
+#pragma unroll
+  for (int v = 0; v < P; ++v) pc[v] = piece_at<W, FIT>(W * (threadIdx.x + v * NT), H);
+  // (only the last pieces of a row can lie past its end: with 16 columns a
+  // thread, those of the last pass)
+  auto own = [&](auto raw, auto type, int v) {
+    using T = decltype(type);
+    if (EPT == 16 && v < P - 1) return raw;
+    return own_cols<T, W, FIT>(raw, pc[v]);
+  };
+  auto gain = [&](const void* p, const V* kept, int v) -> V {
+    if constexpr (KEEP) return kept[v];
+    else return load_gain<W>(p, n.gain_dtype, pc[v].col, H, n.gain_offset);
+  };
+  Raw<YT, W> yq[P];
+  Raw<RT, W> rq[P];
+  Raw<float, 4> eq[P];                 // COMB: the first local slot's row
+  int row = -1, row1 = -1;             // COMB: lane j holds slot j's row and
+  float w = 0.0f, w1 = 0.0f;           //   weight, of this token and the next
+  auto slots = [&](long t, int* rv, float* wv) {
+    *rv = -1;
+    *wv = 0.0f;
+    if (lane < q.c.k && t < n.T) {
+      *rv = q.c.pair_row[t * q.c.k + lane];
+      *wv = q.c.w[t * q.c.k + lane];
+      if (*rv >= q.c.cap) *rv = -1;
+    }
+  };
+  auto expert_row = [&](int r, Raw<float, 4>* e) {
+    const float* yr = q.c.y_perm + (size_t)r * H;
+#pragma unroll
+    for (int v = 0; v < P; ++v) e[v] = load_piece<float, 4, FIT, STREAM>(yr, pc[v], H);
+  };
+  // requests the rows of token t; `row` holds its slots
+  auto fetch = [&](long t) {
     if constexpr (COMB) {
-      if (threadIdx.x < 64) {          // the token's local slots, in order
-        const int j = threadIdx.x;
-        int row = j < q.c.k ? q.c.pair_row[t * q.c.k + j] : -1;
-        const float w = j < q.c.k ? q.c.w[t * q.c.k + j] : 0.0f;
-        if (row >= q.c.cap) row = -1;
-        const uint64_t m = __ballot(row >= 0);
-        if (row >= 0) {
-          const int pos = __popcll(m & ((1ull << j) - 1ull));
-          s_row[par][pos] = row;
-          s_w[par][pos] = w;
-        }
-        if (j == 0) s_n[par] = __popcll(m);
+      const uint64_t m = __ballot(row >= 0);
+      if (m) expert_row(__builtin_amdgcn_readlane(row, __ffsll((unsigned long long)m) - 1), eq);
+      if (q.c.y_shared) {
+#pragma unroll
+        for (int v = 0; v < P; ++v)
+          yq[v] = load_piece<YT, W, FIT, STREAM>((const YT*)q.c.y_shared + t * H, pc[v], H);
       }
+    } else if (q.a.y) {
+#pragma unroll
+      for (int v = 0; v < P; ++v)
+        yq[v] = load_piece<YT, W, FIT, STREAM>((const YT*)q.a.y + t * n.block_stride, pc[v], H);
     }
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-      y[v] = 0.0f;
-      r[v] = 0.0f;
-      if (left <= 0) continue;
-      if constexpr (COMB) {
-        if (q.c.y_shared)
-          y[v] = load8<float, AL>(q.c.y_shared + t * H + col, left);
-      } else if (q.a.y) {
-        y[v] = load8<YT, AL>((const YT*)q.a.y + t * n.block_stride + col, left);
-      }
-      r[v] = load8<RT, AL>(rr + col, left);
+    for (int v = 0; v < P; ++v)
+      rq[v] = load_piece<RT, W, FIT, STREAM>((const RT*)q.a.resid + t * n.resid_stride, pc[v], H);
+  };
+#pragma unroll
+  for (int v = 0; v < P; ++v) yq[v] = 0u;
+  if constexpr (COMB) {
+    slots(blockIdx.x, &row, &w);
+    slots(blockIdx.x + G, &row1, &w1);
+  }
+  if constexpr (KEEP) {
+    fetch(blockIdx.x);
+#pragma unroll
+    for (int v = 0; v < P; ++v) {
+      post[v] = pre[v] = 0.0f;
+      if (q.a.post_gain) post[v] = load_gain<W>(q.a.post_gain, n.gain_dtype, pc[v].col, H, n.gain_offset);
+      if (q.a.pre_gain) pre[v] = load_gain<W>(q.a.pre_gain, n.gain_dtype, pc[v].col, H, n.gain_offset);
+    }
+  }
+  int par = 0;
+  for (long t = blockIdx.x; t < n.T; t += G, par ^= 1) {
+    if constexpr (!KEEP) fetch(t);
+    V y[P], r[P];
+#pragma unroll
+    for (int v = 0; v < P; ++v) {
+      y[v] = widen<YT, W>(own(yq[v], YT{}, v));
+      r[v] = widen<RT, W>(own(rq[v], RT{}, v));
     }
     if constexpr (COMB) {
       // slots in order, then the shared expert, as moe_combine adds them
-      f32x8_t acc[VPT];
+      V acc[P];
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
-      __syncthreads();
-      const int ns = s_n[par];
-      for (int j = 0; j < ns; ++j) {
-        const float* yr = q.c.y_perm + (size_t)s_row[par][j] * H;
-        const float w = s_w[par][j];
+      for (int v = 0; v < P; ++v) acc[v] = 0.0f;
+      auto add = [&](int j, const Raw<float, 4>* e) {
+        const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-          if (left <= 0) continue;
-          const f32x8_t e = load8<float, AL>(yr + col, left);
+        for (int v = 0; v < P; ++v) {
+          const f32x4_t ev = widen<float, 4>(own(e[v], float{}, v));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[v][i] = __builtin_fmaf(w, e[i], acc[v][i]);
+          for (int i = 0; i < 4; ++i) acc[v][i] = __builtin_fmaf(wj, ev[i], acc[v][i]);
         }
+      };
+      uint64_t m = __ballot(row >= 0);
+      if (m) {
+        add(__ffsll((unsigned long long)m) - 1, eq);
+        m &= m - 1;
+      }
+      while (m) {                      // two further rows in flight at a time
+        const int j = __ffsll((unsigned long long)m) - 1;
+        m &= m - 1;
+        const int j2 = m ? __ffsll((unsigned long long)m) - 1 : -1;
+        m &= m - 1;
+        Raw<float, 4> e[P], e2[P];
+        expert_row(__builtin_amdgcn_readlane(row, j), e);
+        if (j2 >= 0) expert_row(__builtin_amdgcn_readlane(row, j2), e2);
+        add(j, e);
+        if (j2 >= 0) add(j2, e2);
       }
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) y[v] = q.c.y_shared ? acc[v] + y[v] : acc[v];
+      for (int v = 0; v < P; ++v) y[v] = q.c.y_shared ? acc[v] + y[v] : acc[v];
+      row = row1;
+      w = w1;
+    }
+    if constexpr (KEEP) {
+      if (t + G < n.T) fetch(t + G);
+    }
+    if constexpr (COMB) {
+      slots(t + 2 * G, &row1, &w1);
       if (q.c.block_out) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-          if (left > 0)
-            store8<YT, AL>((YT*)q.c.block_out + t * n.block_stride + col, y[v], left);
-        }
+        for (int v = 0; v < P; ++v)
+          store_piece_as<W, FIT, STREAM>(n.block_dtype, q.c.block_out, t * n.block_stride, pc[v], H, y[v]);
       }
     }
     if (q.a.post_gain) {
       float s[1] = {0.0f};
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) s[0] += dot8(y[v], y[v]);
-      block_sum(s, red[par][0]);
+      for (int v = 0; v < P; ++v) s[0] += dot_cols<W>(y[v], y[v]);
+      row_sum(s, red[par][0], 0, waves);
       const float rs = 1.0f / sqrtf(s[0] * inv_h + n.eps);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-        if (left <= 0) continue;
-        y[v] = y[v] * rs * load_gain<AL>(q.a.post_gain, n.gain_dtype == MOE_BF16, col, left, n.gain_offset);
-      }
+      for (int v = 0; v < P; ++v) y[v] = y[v] * rs * gain(q.a.post_gain, post, v);
     }
     if (q.a.gate) {
       const float* g = q.a.gate + (n.gate_rows > 1 ? t * n.gate_cols : 0);
       if (n.gate_cols == 1) {
         const float f = g[0];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) y[v] *= f;
+        for (int v = 0; v < P; ++v) y[v] *= f;
       } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-          if (left > 0) y[v] *= load8<float, false>(g + col, left);
-        }
+        for (int v = 0; v < P; ++v) y[v] *= load_f32<W, kAny>(g, pc[v], H);
       }
     }
     float s[1] = {0.0f};
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-      if (left <= 0) continue;
+    for (int v = 0; v < P; ++v) {
       r[v] += n.residual_scale * y[v];
-      s[0] += dot8(r[v], r[v]);
+      s[0] += dot_cols<W>(r[v], r[v]);
       if (q.a.resid_out)
-        store8<RT, AL>((RT*)q.a.resid_out + t * n.resid_out_stride + col, r[v], left);
+        store_piece<RT, W, FIT, STREAM>((RT*)q.a.resid_out + t * n.resid_out_stride, pc[v], H, r[v]);
     }
     if (q.a.x_out) {
-      block_sum(s, red[par][1]);
+      row_sum(s, red[par][1], 0, waves);
       const float rs = 1.0f / sqrtf(s[0] * inv_h + n.eps);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-        if (left <= 0) continue;
-        store8<XT, AL>((XT*)q.a.x_out + t * n.out_stride + col,
-                       r[v] * rs * load_gain<AL>(q.a.pre_gain, n.gain_dtype == MOE_BF16, col, left, n.gain_offset),
-                       left);
-      }
+      for (int v = 0; v < P; ++v)
+        store_piece_as<W, FIT, STREAM>(n.out_dtype, q.a.x_out, t * n.out_stride, pc[v], H,
+                                       r[v] * rs * gain(q.a.pre_gain, pre, v));
     }
   }
 }
 
-// ------------------------------------------------------------ backward
-struct NormGradRun {
-  moe_norm n;
-  NormGradArgs a;
-  float* part;      // [arrays][gridDim.x][H], then [gridDim.x] for a scalar
-  int col_gate;     // the gate's gradient is a column sum
-  int one_gate;     // ... is one number
-};
-
-template <typename YT, typename RT, typename XT, bool AL, int VPT>
-__global__ __launch_bounds__(1024) void k_residual_norm_backward(NormGradRun q) {
-  __shared__ float red[2][2][32];
+template <typename YT, typename RT, int W, bool COMB>
+void launch(const NormRun& q, bool al, bool stream, hipStream_t s) {
   const moe_norm& n = q.n;
-  const NormGradArgs& a = q.a;
-  const int H = n.H, NT = blockDim.x;
-  const float inv_h = 1.0f / (float)H;
-  const bool gain_bf16 = n.gain_dtype == MOE_BF16;
-  f32x8_t d_pre[VPT], d_post[VPT], d_gc[VPT];
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) d_pre[v] = d_post[v] = d_gc[v] = 0.0f;
-  float d_one = 0.0f;
-  int par = 0;
-  for (long t = blockIdx.x; t < n.T; t += gridDim.x, par ^= 1) {
-    f32x8_t g[VPT], r[VPT], x[VPT], y[VPT];
-    float s[2] = {0.0f, 0.0f}, sy = 0.0f;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-      g[v] = r[v] = x[v] = y[v] = 0.0f;
-      if (left <= 0) continue;
-      if (a.d_resid_out)
-        g[v] = load8<RT, AL>((const RT*)a.d_resid_out + t * n.resid_out_stride + col, left);
-      if (a.d_x) {
-        r[v] = load8<RT, AL>((const RT*)a.resid_out + t * n.resid_out_stride + col, left);
-        x[v] = load8<XT, AL>((const XT*)a.d_x + t * n.out_stride + col, left);
-      }
-      if (a.y) y[v] = load8<YT, AL>((const YT*)a.y + t * n.block_stride + col, left);
-    }
-    float rs = 0.0f, ys = 1.0f;
-    f32x8_t gp[VPT];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-      gp[v] = 0.0f;
-      if (left <= 0) continue;
-      if (a.d_x) {
-        gp[v] = x[v] * load_gain<AL>(a.pre_gain, gain_bf16, col, left, n.gain_offset);
-        s[0] += dot8(r[v], r[v]);
-        s[1] += dot8(r[v], gp[v]);
-      }
-      sy += dot8(y[v], y[v]);
-    }
-    float s3[3] = {s[0], s[1], sy};
-    __shared__ float red3[2][48];
-    block_sum(s3, red3[par]);
-    if (a.d_x) {
-      rs = 1.0f / sqrtf(s3[0] * inv_h + n.eps);
-      const float c = s3[1] * inv_h * rs * rs;     // mean(gp r') rs^2
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        g[v] += rs * (gp[v] - c * r[v]);
-        d_pre[v] += x[v] * r[v] * rs;
-      }
-    }
-    if (a.post_gain) ys = 1.0f / sqrtf(s3[2] * inv_h + n.eps);
-    if (a.d_resid) {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-        if (left > 0) store8<RT, AL>((RT*)a.d_resid + t * n.resid_stride + col, g[v], left);
-      }
-    }
-    if (!a.d_y && !a.d_post && !a.d_gate) continue;
-    // g: the gradient of residual_scale * gate * v from here on
-    float sums[2] = {0.0f, 0.0f};    // gate's row sum, mean of the post-norm
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-      if (left <= 0) continue;
-      f32x8_t pg;
-      pg = 1.0f;
-      if (a.post_gain) pg = load_gain<AL>(a.post_gain, gain_bf16, col, left, n.gain_offset);
-      g[v] *= n.residual_scale;
-      if (a.gate) {
-        const float* gt = a.gate + (n.gate_rows > 1 ? t * n.gate_cols : 0);
-        const f32x8_t e = g[v] * (y[v] * ys * pg);
-        if (n.gate_cols == 1) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sums[0] += e[i];
-          g[v] *= gt[0];
-        } else {
-          if (q.col_gate) d_gc[v] += e;
-          else if (a.d_gate) store8<float, false>(a.d_gate + t * H + col, e, left);
-          g[v] *= load8<float, false>(gt + col, left);
-        }
-      }
-      if (a.post_gain) {
-        d_post[v] += g[v] * y[v] * ys;
-        g[v] *= pg;
-        sums[1] += dot8(g[v], y[v]);
-      }
-    }
-    if (a.post_gain || (a.d_gate && n.gate_cols == 1)) block_sum(sums, red[par][0]);
-    if (a.d_gate && n.gate_cols == 1) {
-      if (q.one_gate) d_one += sums[0];
-      else if (threadIdx.x == 0) a.d_gate[t] = sums[0];
-    }
-    if (a.d_y) {
-      const float c = sums[1] * inv_h * ys * ys;
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-        if (left <= 0) continue;
-        if (a.post_gain) g[v] = ys * (g[v] - c * y[v]);
-        store8<YT, AL>((YT*)a.d_y + t * n.block_stride + col, g[v], left);
-      }
-    }
-  }
-  float* part = q.part + (size_t)blockIdx.x * H;
-  const size_t step = (size_t)gridDim.x * H;
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int col = 8 * (threadIdx.x + v * NT), left = H - col;
-    if (left <= 0) continue;
-    float* p = part + col;
-    if (a.d_pre) { store8<float, false>(p, d_pre[v], left); p += step; }
-    if (a.d_post) { store8<float, false>(p, d_post[v], left); p += step; }
-    if (q.col_gate) store8<float, false>(p, d_gc[v], left);
-  }
-  if (q.one_gate && threadIdx.x == 0) {
-    const int arrays = (a.d_pre ? 1 : 0) + (a.d_post ? 1 : 0);
-    q.part[arrays * step + blockIdx.x] = d_one;
+  // Columns a thread: 8 where a row then fits 512 threads (combine + norm,
+  // which holds three rows: 1024; 8192 x 7168 146 us against 167 us at 16).
+  // By H alone: a row's sums have the same order whatever the batch.
+  const int v = (n.H + 7) / 8;
+  const int ept = v <= (COMB ? 1024 : 512) ? 8 : 16;
+  const bool keep = ept == 8 || v <= 1024;
+  const int nt = ((n.H + ept - 1) / ept + 63) / 64 * 64;
+  // the workgroups that stay on the GPU at once, at 16 wavefronts a CU
+  const int per_cu = std::max(1, 16 / (nt / 64));
+  const dim3 grid(std::min(n.T, 256 * per_cu)), block(nt);
+  auto go = [&](auto alt, auto st) {
+    constexpr Fit A = alt.value ? kAligned : kAny;
+    constexpr bool S = st.value;
+    if (ept == 8) k_residual_norm<YT, RT, W, A, 8, COMB, S, true><<<grid, block, 0, s>>>(q);
+    else if (keep) k_residual_norm<YT, RT, W, A, 16, COMB, S, true><<<grid, block, 0, s>>>(q);
+    else k_residual_norm<YT, RT, W, A, 16, COMB, S, false><<<grid, block, 0, s>>>(q);
+  };
+  if constexpr (W == 8) {              // only rows that are aligned
+    by_flag(stream, [&](auto st) { go(std::true_type{}, st); });
+  } else {
+    if (!al) go(std::false_type{}, std::false_type{});
+    else by_flag(stream, [&](auto st) { go(std::true_type{}, st); });
   }
 }
-
-// out[c] = sum over the workgroups' partial sums, in a fixed order
-struct ColumnSums {
-  const float* part[3];
-  float* out[3];
-};
-
-__global__ __launch_bounds__(256) void k_column_sums(ColumnSums q, int parts,
-                                                     int H) {
-  __shared__ float s[4][64];
-  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + c;
-  const float* part = q.part[blockIdx.y];
-  double v = 0.0;
-  if (col < H)
-    for (int p = w; p < parts; p += 4) v += (double)part[(size_t)p * H + col];
-  s[w][c] = (float)v;
-  __syncthreads();
-  if (w == 0 && col < H)
-    q.out[blockIdx.y][col] = (s[0][c] + s[1][c]) + (s[2][c] + s[3][c]);
-}
-
-__global__ __launch_bounds__(64) void k_one_sum(const float* part, int parts,
-                                                float* out) {
-  double v = 0.0;
-  for (int p = threadIdx.x; p < parts; p += 64) v += (double)part[p];
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  if (threadIdx.x == 0) *out = (float)v;
-}
-
-__global__ __launch_bounds__(256) void k_clear(float* p, long n) {
-  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += 256l * gridDim.x) p[i] = 0.0f;
-}
-
-bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-
-// rows of `stride` elements can move as whole 16-byte pieces
-bool rows_aligned(const void* p, int dtype, int64_t stride) {
-  return !p || (al16(p) && stride % (dtype == MOE_BF16 ? 8 : 4) == 0);
-}
-
-// threads and passes for a row of H columns
-int row_threads(int H, int* vpt) {
-  const int v = (H + 7) / 8;
-  *vpt = v <= 1024 ? 1 : 2;
-  const int nt = (v + *vpt - 1) / *vpt;
-  return (nt + 63) / 64 * 64;
-}
-
-template <class F>
-void by_type(int dtype, F f) {
-  if (dtype == MOE_BF16) f(bf16_t{});
-  else f(float{});
-}
-
-template <class F>
-void by_flag(bool b, F f) {
-  if (b) f(std::true_type{});
-  else f(std::false_type{});
-}
-
-int norm_grad_grid(int T) { return T < 512 ? T : 512; }
 
 }  // namespace
 
@@ -468,96 +238,32 @@ hipError_t launch_residual_norm(const moe_norm* n, const NormArgs& a,
   q.n = *n;
   q.a = a;
   if (comb) q.c = *comb;
-  bool al = n->H % 8 == 0 && rows_aligned(a.y, n->block_dtype, n->block_stride) &&
-            rows_aligned(a.resid, n->resid_dtype, n->resid_stride) &&
-            rows_aligned(a.resid_out, n->resid_dtype, n->resid_out_stride) &&
-            rows_aligned(a.x_out, n->out_dtype, n->out_stride) &&
-            al16(a.post_gain) && al16(a.pre_gain);
-  if (comb)
-    al = al && al16(comb->y_perm) && al16(comb->y_shared) &&
-         rows_aligned(comb->block_out, n->block_dtype, n->block_stride);
-  int vpt;
-  const dim3 block(row_threads(n->H, &vpt));
-  const dim3 grid(n->T < (1 << 20) ? n->T : (1 << 20));
-  by_type(n->block_dtype, [&](auto yt) {
+  auto aligned = [&](int W) {
+    return n->H % W == 0 && rows_aligned(a.y, n->block_dtype, n->block_stride, W) &&
+           rows_aligned(a.resid, n->resid_dtype, n->resid_stride, W) &&
+           rows_aligned(a.resid_out, n->resid_dtype, n->resid_out_stride, W) &&
+           rows_aligned(a.x_out, n->out_dtype, n->out_stride, W) &&
+           rows_aligned(q.c.block_out, n->block_dtype, n->block_stride, W);
+  };
+  // Rows that do not fit the caches pass them by: norm of 8192 x 7168 84 us
+  // against 92 us, combine + norm 146 us against 159 us; a decode batch of
+  // 128, whose rows the caches hold, 6.0 us against 8.2 us with the hint.
+  const bool stream = (double)n->T * n->H * 8 >= 64.0 * 1048576.0;
+  const bool al4 = aligned(4);
+  if (comb) {
     by_type(n->resid_dtype, [&](auto rt) {
-      by_type(n->out_dtype, [&](auto xt) {
-        by_flag(al, [&](auto alt) {
-          by_flag(comb != nullptr, [&](auto cb) {
-            using Y = decltype(yt);
-            using R = decltype(rt);
-            using X = decltype(xt);
-            if (vpt == 1)
-              k_residual_norm<Y, R, X, alt.value, 1, cb.value><<<grid, block, 0, s>>>(q);
-            else
-              k_residual_norm<Y, R, X, alt.value, 2, cb.value><<<grid, block, 0, s>>>(q);
-          });
-        });
+      launch<float, decltype(rt), 4, true>(q, al4, stream, s);
+    });
+  } else if (n->block_dtype == MOE_BF16 && n->resid_dtype == MOE_BF16 &&
+             n->out_dtype == MOE_BF16 && aligned(8)) {
+    launch<bf16_t, bf16_t, 8, false>(q, true, stream, s);
+  } else {
+    by_type(n->block_dtype, [&](auto yt) {
+      by_type(n->resid_dtype, [&](auto rt) {
+        launch<decltype(yt), decltype(rt), 4, false>(q, al4, stream, s);
       });
     });
-  });
-  return hipGetLastError();
-}
-
-size_t norm_grad_partials(const moe_norm* n) {
-  return (size_t)norm_grad_grid(n->T) * (3 * (size_t)n->H + 1);
-}
-
-hipError_t launch_residual_norm_backward(const moe_norm* n,
-                                         const NormGradArgs& a,
-                                         float* partials, hipStream_t s) {
-  const bool gate_row = a.gate && n->gate_rows == 1;
-  NormGradRun q{};
-  q.n = *n;
-  q.a = a;
-  q.part = partials;
-  q.one_gate = a.d_gate && gate_row && n->gate_cols == 1;
-  q.col_gate = a.d_gate && gate_row && n->gate_cols > 1;
-  const size_t H = n->H;
-  if (n->T == 0) {
-    if (!a.d_pre && !a.d_post && !q.one_gate && !q.col_gate) return hipSuccess;
-    if (a.d_pre) k_clear<<<64, 256, 0, s>>>(a.d_pre, H);
-    if (a.d_post) k_clear<<<64, 256, 0, s>>>(a.d_post, H);
-    if (q.one_gate || q.col_gate) k_clear<<<64, 256, 0, s>>>(a.d_gate, n->gate_cols);
-    return hipGetLastError();
   }
-  const bool al = n->H % 8 == 0 && rows_aligned(a.y, n->block_dtype, n->block_stride) &&
-                  rows_aligned(a.d_y, n->block_dtype, n->block_stride) &&
-                  rows_aligned(a.resid_out, n->resid_dtype, n->resid_out_stride) &&
-                  rows_aligned(a.d_resid_out, n->resid_dtype, n->resid_out_stride) &&
-                  rows_aligned(a.d_resid, n->resid_dtype, n->resid_stride) &&
-                  rows_aligned(a.d_x, n->out_dtype, n->out_stride) &&
-                  al16(a.post_gain) && al16(a.pre_gain);
-  int vpt;
-  const dim3 block(row_threads(n->H, &vpt)), grid(norm_grad_grid(n->T));
-  by_type(n->block_dtype, [&](auto yt) {
-    by_type(n->resid_dtype, [&](auto rt) {
-      by_type(n->out_dtype, [&](auto xt) {
-        by_flag(al, [&](auto alt) {
-          using Y = decltype(yt);
-          using R = decltype(rt);
-          using X = decltype(xt);
-          if (vpt == 1)
-            k_residual_norm_backward<Y, R, X, alt.value, 1><<<grid, block, 0, s>>>(q);
-          else
-            k_residual_norm_backward<Y, R, X, alt.value, 2><<<grid, block, 0, s>>>(q);
-        });
-      });
-    });
-  });
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  ColumnSums c{};
-  int arrays = 0;
-  const size_t step = (size_t)grid.x * H;
-  for (float* out : {a.d_pre, a.d_post, q.col_gate ? a.d_gate : nullptr})
-    if (out) {
-      c.part[arrays] = partials + arrays * step;
-      c.out[arrays++] = out;
-    }
-  if (arrays)
-    k_column_sums<<<dim3((n->H + 63) / 64, arrays), 256, 0, s>>>(c, grid.x, n->H);
-  if (q.one_gate) k_one_sum<<<1, 64, 0, s>>>(partials + arrays * step, grid.x, a.d_gate);
   return hipGetLastError();
 }
 
