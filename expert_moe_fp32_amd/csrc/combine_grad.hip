@@ -7,68 +7,83 @@
 #include <type_traits>
 
 #include "block.h"
+#include "rows.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 4 * kThreads;       // columns of one pass
+constexpr int kPieces = 4;                     // pieces of 4 columns a thread
+constexpr int kCols = 4 * kThreads * kPieces;  // columns of one pass
 
-template <typename T>
-__device__ __forceinline__ f32x4_t load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *(const f32x4_t*)p;
-  } else {
-    typedef __attribute__((ext_vector_type(2))) uint32_t u2;
-    const u2 u = *(const u2*)p;
-    return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                   __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
-  }
-}
-
-template <typename T>
+// Every wavefront holds the token's slots in its lanes, so the walk over the
+// local ones needs no exchange.  A pass's pieces of d_out and of a slot's row
+// are requested together; rows are read and written once, past the caches in
+// a batch that does not fit them (STREAM).
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(
     const T* __restrict__ d_out, const float* __restrict__ y_perm,
     const int32_t* __restrict__ pair_row, const float* __restrict__ w, int T_,
     int H, int k, int cap, float* __restrict__ d_y_perm,
     float* __restrict__ d_w, float* __restrict__ d_y_shared) {
-  __shared__ float part[4][MOE_KMAX];
+  __shared__ float part[2][4][MOE_KMAX];       // by token parity
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (long t = blockIdx.x; t < T_; t += gridDim.x) {
-    __syncthreads();
-    if (threadIdx.x < 4 * MOE_KMAX) part[0][threadIdx.x] = 0.0f;
-    __syncthreads();
+  int par = 0;
+  for (long t = blockIdx.x; t < T_; t += gridDim.x, par ^= 1) {
+    int row = -1;
+    float wt = 0.0f;
+    if (lane < k) {
+      row = pair_row[t * k + lane];
+      wt = w[t * k + lane];
+      if (row >= cap) row = -1;
+    }
+    float sums = 0.0f;                         // lane j: slot j, this wavefront's columns
     for (int c0 = 0; c0 < H; c0 += kCols) {
-      const int col = c0 + 4 * threadIdx.x;
-      f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-      if (col < H) {
-        d = load4<T>(d_out + t * H + col);
-        if (d_y_shared) *(f32x4_t*)(d_y_shared + t * H + col) = d;
-      }
-      for (int j = 0; j < k; ++j) {
-        const int row = pair_row[t * k + j];
-        if (row < 0 || row >= cap) continue;
-        const float wj = w[t * k + j];
-        float s = 0.0f;
-        if (col < H) {
-          if (d_w) {
-            const f32x4_t y = *(const f32x4_t*)(y_perm + (size_t)row * H + col);
-            s = d.x * y.x + d.y * y.y + d.z * y.z + d.w * y.w;
-          }
-          if (d_y_perm) *(f32x4_t*)(d_y_perm + (size_t)row * H + col) = wj * d;
-        }
-        if (d_w) {
+      Piece pc[kPieces];
+      f32x4_t d[kPieces];
 #pragma unroll
-          for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
-          if (lane == 0) part[wv][j] += s;
+      for (int v = 0; v < kPieces; ++v) {
+        pc[v] = piece_at<4, kAligned>(c0 + 4 * (threadIdx.x + v * kThreads), H);
+        d[v] = widen<T, 4>(own_cols<T, 4, kAligned>(
+            load_piece<T, 4, kAligned, STREAM>(d_out + t * H, pc[v], H), pc[v]));
+      }
+      uint64_t m = __ballot(row >= 0);
+      while (m) {
+        const int j = __ffsll((unsigned long long)m) - 1;
+        m &= m - 1;
+        const size_t at = (size_t)__builtin_amdgcn_readlane(row, j) * H;
+        if (d_w) {
+          f32x4_t y[kPieces];
+#pragma unroll
+          for (int v = 0; v < kPieces; ++v)
+            y[v] = widen<float, 4>(own_cols<float, 4, kAligned>(
+                load_piece<float, 4, kAligned, STREAM>(y_perm + at, pc[v], H), pc[v]));
+          float s = 0.0f;
+#pragma unroll
+          for (int v = 0; v < kPieces; ++v) s += dot_cols<4>(d[v], y[v]);
+          s = wave_sum(s);
+          if (lane == j) sums += s;
         }
+        if (d_y_perm) {
+          const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wt), j));
+#pragma unroll
+          for (int v = 0; v < kPieces; ++v)
+            store_piece<float, 4, kAligned, STREAM>(d_y_perm + at, pc[v], H, wj * d[v]);
+        }
+      }
+      if (d_y_shared) {
+#pragma unroll
+        for (int v = 0; v < kPieces; ++v)
+          store_piece<float, 4, kAligned, STREAM>(d_y_shared + t * H, pc[v], H, d[v]);
       }
     }
-    __syncthreads();
-    if (d_w && threadIdx.x < k) {
-      const int j = threadIdx.x;
-      d_w[t * k + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
+    if (d_w) {
+      if (lane < k) part[par][wv][lane] = sums;
+      lds_barrier();
+      if (threadIdx.x < k)
+        d_w[t * k + lane] = (part[par][0][lane] + part[par][1][lane]) +
+                            (part[par][2][lane] + part[par][3][lane]);
     }
   }
 }
@@ -82,14 +97,15 @@ hipError_t launch_combine_backward(const void* d_out, int out_dtype,
                                    float* d_y_perm, float* d_w,
                                    float* d_y_shared, hipStream_t s) {
   const dim3 grid(T < (1 << 20) ? T : (1 << 20));
-  if (out_dtype == MOE_BF16)
-    k_combine_backward<bf16_t><<<grid, kThreads, 0, s>>>(
-        (const bf16_t*)d_out, y_perm, pair_row, w, T, H, k, cap, d_y_perm, d_w,
-        d_y_shared);
-  else
-    k_combine_backward<float><<<grid, kThreads, 0, s>>>(
-        (const float*)d_out, y_perm, pair_row, w, T, H, k, cap, d_y_perm, d_w,
-        d_y_shared);
+  const bool stream = (double)T * H * 8 >= 64.0 * 1048576.0;
+  by_type(out_dtype, [&](auto type) {
+    using D = decltype(type);
+    by_flag(stream, [&](auto st) {
+      k_combine_backward<D, st.value><<<grid, kThreads, 0, s>>>(
+          (const D*)d_out, y_perm, pair_row, w, T, H, k, cap, d_y_perm, d_w,
+          d_y_shared);
+    });
+  });
   return hipGetLastError();
 }
 

@@ -2,12 +2,24 @@
 //
 // A token's experts lie on a segment of 16 lanes (E <= 64, four tokens a
 // wavefront) or a whole wavefront, EPL neighbouring experts a lane, so the
-// lowest lane among equal values holds the lowest id.  Scores, choices and
-// group scores are doubles: the chosen ids must be those of the definition,
-// and in float32 neighbouring choices of some hundred experts collide within
-// an ulp too often.  On this card a double operation issues at the rate of an
-// unpacked float one.
+// lowest lane among equal values holds the lowest id.
+//
+// The chosen ids must be those of the definition in 64 bits, and in float32
+// neighbouring choices of some hundred experts collide within an ulp too
+// often.  So a token is chosen in float32, the scores of the k chosen (which
+// the weights need) are evaluated in double, and these prove the choice:
+//   - the doubles stand in slot order (equal ones by id), and
+//   - the last of them exceeds the best choice left behind by more than a
+//     bound on float32's error, and likewise the last group that stays
+//     exceeds the best that does not.
+// The few tokens without that proof are chosen again in double throughout.
+//
+// Each lane sorts its few choices as integer keys in the order of the
+// choices; a slot is then one max over the lanes' first keys in DPP steps of
+// one instruction, and the owner moves its list up.  Bound by instructions
+// and, for single tokens, by their latency.
 #include <float.h>
+#include <algorithm>
 #include <type_traits>
 
 #include "block.h"
@@ -16,19 +28,43 @@ namespace moe {
 
 namespace {
 
-// An expert's choice: live values, kMasked for masked experts, and kGone for
-// experts that are taken, outside the groups that stay, or padding.
+// Choice of a masked expert, below every live one.
 constexpr double kMasked = -DBL_MAX;
-#define kGone (-__builtin_inf())
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp(double old, double v) {
-  const uint64_t o = __double_as_longlong(old), b = __double_as_longlong(v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp((int)(o >> 32), (int)(b >> 32), CTRL, ROWS, 0xF, false);
-  return __longlong_as_double(((uint64_t)hi << 32) | lo);
+// Keys order as choices do: the bits of a double mapped to an unsigned order.
+// Masked experts are all equal and come last; kGone is what is taken, outside
+// the groups that stay, or padding.
+constexpr uint64_t kMaskedKey = 1ull << 32, kGone = 0;
+__device__ __forceinline__ uint64_t key_of(double c) {
+  const uint64_t b = __double_as_longlong(c);
+  return c == kMasked ? kMaskedKey : (b >> 63 ? ~b : b | (1ull << 63));
 }
 
+// A DPP move within rows of 16 lanes, every lane written (a lane without a
+// source gets 0): no old value, so the compiler folds it into the operation.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return __builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  return __longlong_as_double(((uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32) | dpp<CTRL>((uint32_t)b));
+}
+// The row broadcasts: lane 15 (CTRL 0x142) or 31 (0x143) of the rows before
+// into the rows of the mask, 0 elsewhere.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t bcast(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
 __device__ __forceinline__ double read_lane(double v, int lane) {
   const uint64_t b = __double_as_longlong(v);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
@@ -40,53 +76,67 @@ __device__ __forceinline__ double read_lane(double v, int lane) {
 // rotations by 8, 4, 2, 1 leave a row's result in its 16 lanes; row
 // broadcasts carry it on to lane 63.
 template <int LANES>
-__device__ __forceinline__ double seg_max(double v) {
-  v = fmax(v, dpp<0x128, 0xF>(v, v));
-  v = fmax(v, dpp<0x124, 0xF>(v, v));
-  v = fmax(v, dpp<0x122, 0xF>(v, v));
-  v = fmax(v, dpp<0x121, 0xF>(v, v));
+__device__ __forceinline__ uint32_t seg_max(uint32_t v) {
+  v = max(v, dpp<0x128>(v));
+  v = max(v, dpp<0x124>(v));
+  v = max(v, dpp<0x122>(v));
+  v = max(v, dpp<0x121>(v));
   if (LANES == 64) {
-    v = fmax(v, dpp<0x142, 0xA>(v, v));
-    v = fmax(v, dpp<0x143, 0xC>(v, v));
-    v = read_lane(v, 63);
+    v = max(v, bcast<0x142, 0xA>(v));
+    v = max(v, bcast<0x143, 0xC>(v));
+    v = __builtin_amdgcn_readlane((int)v, 63);
   }
   return v;
 }
+// floats as unsigned integers of the same order
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_order(uint32_t m) {
+  return __uint_as_float(m >> 31 ? m & 0x7FFFFFFFu : ~m);
+}
+template <int LANES>
+__device__ __forceinline__ float seg_max(float v) {
+  return from_order(seg_max<LANES>(order_of(v)));
+}
 
+// sum over the 16 lanes of a row / over a segment, in every lane of it
+__device__ __forceinline__ double row_sum(double v) {
+  v += dpp<0x128>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  return v + dpp<0x121>(v);
+}
 template <int LANES>
 __device__ __forceinline__ double seg_sum(double v) {
-  v += dpp<0x128, 0xF>(0.0, v);
-  v += dpp<0x124, 0xF>(0.0, v);
-  v += dpp<0x122, 0xF>(0.0, v);
-  v += dpp<0x121, 0xF>(0.0, v);
-  if (LANES == 64) {
-    v += dpp<0x142, 0xA>(0.0, v);
-    v += dpp<0x143, 0xC>(0.0, v);
-    v = read_lane(v, 63);
-  }
+  v = row_sum(v);
+  if (LANES == 64)
+    v = (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
   return v;
 }
 
-// first lane of the segment at `base` whose predicate holds (it does in one)
-template <int LANES>
-__device__ __forceinline__ int seg_first(bool p, int base) {
-  const uint64_t m = __ballot(p);
-  if (LANES == 64) return __ffsll((unsigned long long)m) - 1;
-  return base + __ffs((int)((m >> base) & 0xFFFFu)) - 1;
-}
-
-template <typename LT>
-__device__ __forceinline__ double to_f64(LT v);
-template <>
-__device__ __forceinline__ double to_f64<float>(float v) { return (double)v; }
-template <>
-__device__ __forceinline__ double to_f64<bf16_t>(bf16_t v) { return (double)bf16_to_f32(v); }
-
 // a logit, with NaN read as -inf
-template <typename LT>
-__device__ __forceinline__ double logit_of(LT v) {
-  const double l = to_f64<LT>(v);
-  return l == l ? l : -__builtin_inf();
+__device__ __forceinline__ float logit_of(float v) { return v == v ? v : -__builtin_inff(); }
+__device__ __forceinline__ float logit_of(bf16_t v) { return logit_of(bf16_to_f32(v)); }
+
+// N logits at `p`; VEC: N * sizeof(LT) bytes aligned to 16 or to their size
+template <int N, bool VEC, typename LT>
+__device__ __forceinline__ void load_logits(const LT* p, int n, float* l) {
+  if (VEC && n >= N) {
+    constexpr int B = N * (int)sizeof(LT) < 16 ? N * (int)sizeof(LT) : 16;
+    struct alignas(B) Block { LT v[B / sizeof(LT)]; };
+    constexpr int M = B / sizeof(LT);
+#pragma unroll
+    for (int j = 0; j < N / M; ++j) {
+      const Block b = ((const Block*)p)[j];
+#pragma unroll
+      for (int i = 0; i < M; ++i) l[j * M + i] = logit_of(b.v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = i < n ? logit_of(p[i]) : -__builtin_inff();
+  }
 }
 
 __device__ __forceinline__ double sigmoid_f64(double l) {
@@ -105,134 +155,389 @@ struct RouteArgs {
   const void* logits;
   const float* bias;
   int T, E, k, sigmoid, groups, keep, group_top, renorm, per;
+  int vec, bias_vec;      // logits / bias rows load as vectors
+  int spread;             // lanes a group, when groups are runs of whole
+                          // lanes, 2^n of them up to 16; else 0
   uint32_t per_inv;       // e / per == (e * per_inv) >> 20 for e < 1024
   float scale;
   int64_t stride;
   int32_t* ids;
   float* w;
+  int32_t* counts;        // or null: [gridDim.x][E], each workgroup's pairs
 };
 
-constexpr int kWaves = 4;   // wavefronts a workgroup
+constexpr int kWaves = 8;   // wavefronts a workgroup
+
+__device__ __forceinline__ double max_of(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double min_of(double a, double b) { return fmin(a, b); }
+__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float min_of(float a, float b) { return fminf(a, b); }
+
+// the best two of two pairs of best ones, the second in another lane
+template <int CTRL, typename V>
+__device__ __forceinline__ void merge_best(V& a0, V& a1) {
+  const V b0 = dpp<CTRL>(a0), b1 = dpp<CTRL>(a1);
+  a1 = max_of(min_of(a0, b0), max_of(a1, b1));
+  a0 = max_of(a0, b0);
+}
+
+// whether group g of score v is among the `keep` best; score(h) is group h's
+template <class F>
+__device__ __forceinline__ bool group_stays(int g, double v, int groups, int keep, F score) {
+  int better = 0;
+  for (int h = 0; h < groups; ++h) {
+    const double s = score(h);
+    better += (s > v || (s == v && h < g)) ? 1 : 0;
+  }
+  return better < keep;
+}
+template <class F>
+__device__ __forceinline__ bool group_stays(int g, float v, int groups, int keep, F score) {
+  // of equal scores the lower group's is above: order(v) less 1
+  const uint32_t o = order_of(v);
+  int better = 0;
+  for (int h = 0; h < groups; ++h)
+    better += order_of(score(h)) > (h < g ? o - 1 : o) ? 1 : 0;
+  return better < keep;
+}
+
+// orders the scratch accesses of one wavefront's lanes
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Clears the keys of the experts whose group does not stay; V: float or double.  Groups of whole lanes by mirrored lanes,
+// others through `scratch` (LANES * EPL + 64 values of one token).
+// For float *gap is the distance of the last group that stays from the best
+// that does not, and *big the largest choice's magnitude; gap = +inf where
+// the border lies at groups without a live expert.
+template <int LANES, int EPL, typename V, typename K>
+__device__ __forceinline__ void stay_mask(const RouteArgs& a, const V* c, K* key,
+                                          V masked, int r, int base,
+                                          double* scratch, float* gap,
+                                          float* big) {
+  const int e0 = r * EPL;
+  V score;
+  bool stays;
+  if (a.spread) {
+    V b0 = masked, b1 = masked;                 // the group's two best
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      b1 = max_of(b1, min_of(b0, c[i]));
+      b0 = max_of(b0, c[i]);
+    }
+    if (a.spread >= 2) merge_best<0xB1>(b0, b1);     // lanes 1 0 3 2
+    if (a.spread >= 4) merge_best<0x4E>(b0, b1);     // lanes 2 3 0 1
+    if (a.spread >= 8) merge_best<0x141>(b0, b1);    // half row mirrored
+    if (a.spread >= 16) merge_best<0x140>(b0, b1);   // row mirrored
+    score = (a.group_top == 2 && b1 > masked) ? b0 + b1 : b0;
+    const int g = r / a.spread;
+    stays = group_stays(g, score, a.groups, a.keep, [&](int h) {
+      if (LANES == 64) return read_lane(score, h * a.spread);
+      return (V)__shfl(score, base + h * a.spread, 64);
+    });
+    if (g >= a.groups) score = masked;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = stays ? key[i] : K(0);
+    if (gap) *big = fmaxf(b0 > masked ? fabsf((float)b0) : 0.0f, b1 > masked ? fabsf((float)b1) : 0.0f);
+    if (gap) {
+      const float s32 = score > masked ? (float)score : -__builtin_inff();
+      const float low = seg_max<LANES>(stays && score > masked ? -s32 : -__builtin_inff());
+      const float next = seg_max<LANES>(stays ? -__builtin_inff() : s32);
+      *gap = next == -__builtin_inff() ? __builtin_inff() : -low - next;
+      *big = seg_max<LANES>(*big);
+    }
+    return;
+  }
+  V* ch = (V*)scratch;
+  V* gs = ch + LANES * EPL;
+  wave_fence();
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) ch[e0 + i] = c[i];
+  wave_fence();
+  float most = 0.0f;
+  for (int g = r; g < a.groups; g += LANES) {
+    V b0 = masked, b1 = masked;
+    for (int i = 0; i < a.per; ++i) {
+      const V v = ch[g * a.per + i];
+      b1 = max_of(b1, min_of(b0, v));
+      b0 = max_of(b0, v);
+    }
+    gs[g] = (a.group_top == 2 && b1 > masked) ? b0 + b1 : b0;
+    if (b0 > masked) most = fmaxf(most, fabsf((float)b0));
+    if (b1 > masked) most = fmaxf(most, fabsf((float)b1));
+  }
+  wave_fence();
+  uint64_t kept = 0;
+  float low = -__builtin_inff(), next = -__builtin_inff();
+  for (int g = r; g < a.groups; g += LANES) {
+    const V v = gs[g];
+    const bool in = group_stays(g, v, a.groups, a.keep, [&](int h) { return gs[h]; });
+    if (in) kept |= 1ull << g;
+    if (v > masked) {
+      if (in) low = fmaxf(low, -(float)v);
+      else next = fmaxf(next, (float)v);
+    }
+  }
+#pragma unroll
+  for (int s = 1; s < LANES; s <<= 1) {
+    const uint32_t lo = __shfl_xor((uint32_t)kept, s, 64);
+    const uint32_t hi = __shfl_xor((uint32_t)(kept >> 32), s, 64);
+    kept |= ((uint64_t)hi << 32) | lo;
+  }
+  if (gap) {
+    low = seg_max<LANES>(low);
+    next = seg_max<LANES>(next);
+    *gap = next == -__builtin_inff() ? __builtin_inff() : -low - next;
+    *big = seg_max<LANES>(most);
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const uint32_t g = ((uint32_t)(e0 + i) * a.per_inv) >> 20;
+    if (!((kept >> (g & 63)) & 1)) key[i] = K(0);
+  }
+}
+
+// A lane's keys in descending order, equal ones by id: neighbours only swap
+// where the right one is larger.
+template <int EPL, typename K>
+__device__ __forceinline__ void sort_keys(K* key, uint32_t* id) {
+#pragma unroll
+  for (int n = EPL - 1; n > 0; --n) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool up = key[i + 1] > key[i];
+      const K hk = up ? key[i + 1] : key[i], lk = up ? key[i] : key[i + 1];
+      const uint32_t hi = up ? id[i + 1] : id[i], li = up ? id[i] : id[i + 1];
+      key[i] = hk;
+      key[i + 1] = lk;
+      id[i] = hi;
+      id[i + 1] = li;
+    }
+  }
+}
+
+// the lanes whose first key is the largest of their segment
+template <int LANES>
+__device__ __forceinline__ uint64_t lanes_of_max(uint32_t key) {
+  return __ballot(key == seg_max<LANES>(key));
+}
+template <int LANES>
+__device__ __forceinline__ uint64_t lanes_of_max(uint64_t key) {
+  const uint32_t hi = (uint32_t)(key >> 32);
+  const uint64_t m = __ballot(hi == seg_max<LANES>(hi));
+  if (__popcll(m) <= 64 / LANES) return m;
+  // upper halves tie somewhere: the lower ones decide
+  const uint32_t lo = (m >> (threadIdx.x & 63)) & 1 ? (uint32_t)key : 0u;
+  return m & __ballot(lo == seg_max<LANES>(lo));
+}
+
+// The k largest keys of a segment's experts (lane r's are r * EPL + i): lane
+// j < k gets the id of slot j; *left becomes the largest key that stays.  Up
+// to 8 keys of 32 bits or 4 of 64 a lane are sorted first; more are scanned in
+// every round, which needs no second array (sorting 16 spilled registers).
+template <int LANES, int EPL, typename K>
+__device__ __forceinline__ int take_slots(K* key, int k, int r, int base, K* left) {
+  constexpr bool kSort = EPL * sizeof(K) <= 32;
+  uint32_t id[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) id[i] = r * EPL + i;
+  if constexpr (kSort) sort_keys<EPL>(key, id);
+  int my_id = 0;
+  for (int j = 0;; ++j) {
+    K head = key[0];
+    uint32_t head_id = id[0];
+    if constexpr (!kSort) {
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) {
+        const bool up = key[i] > head;
+        head = up ? key[i] : head;
+        head_id = up ? r * EPL + i : head_id;
+      }
+    }
+    if (j == k) {
+      *left = head;
+      break;
+    }
+    const uint64_t first = lanes_of_max<LANES>(head);
+    int owner, e;
+    if (LANES == 64) {
+      owner = __ffsll((unsigned long long)first) - 1;
+      e = __builtin_amdgcn_readlane((int)head_id, owner);
+    } else {
+      owner = base + __ffs((int)((first >> base) & 0xFFFFu)) - 1;
+      e = __shfl((int)head_id, owner, 64);
+    }
+    if (r == j) my_id = e;
+    if constexpr (kSort) {
+      const bool mine = (int)(threadIdx.x & 63) == owner;
+#pragma unroll
+      for (int i = 0; i + 1 < EPL; ++i) {
+        key[i] = mine ? key[i + 1] : key[i];
+        id[i] = mine ? id[i + 1] : id[i];
+      }
+      key[EPL - 1] = mine ? K(0) : key[EPL - 1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = r * EPL + i == e ? K(0) : key[i];
+    }
+  }
+  return my_id;
+}
 
 template <int LANES, int EPL, typename LT>
 __global__ __launch_bounds__(64 * kWaves) void k_route_scored(RouteArgs a) {
   constexpr int SEGS = 64 / LANES;
-  __shared__ double lds_c[kWaves][SEGS][LANES * EPL];
-  __shared__ double lds_g[kWaves][SEGS][64];
+  const float kInf = __builtin_inff();
+  extern __shared__ double lds_groups[];   // groups of any size: a token's
+  __shared__ int32_t hist[MOE_EMAX];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = lane & (LANES - 1), seg = lane / LANES, base = seg * LANES;
-  const int E = a.E, k = a.k;
-  const int per_block = kWaves * SEGS;
-  for (long t0 = (long)blockIdx.x * per_block; t0 < a.T;
-       t0 += (long)gridDim.x * per_block) {
-    const long tt = t0 + wv * SEGS + seg;
-    const bool valid = tt < a.T;
-    const long t = valid ? tt : a.T - 1;
-    const LT* row = (const LT*)a.logits + t * a.stride;
-    double l[EPL], c[EPL];
+  const int E = a.E, k = a.k, e0 = r * EPL;
+  const int waves = blockDim.x >> 6, per_block = waves * SEGS;
+  double* scratch = lds_groups + (wv * SEGS + seg) * (LANES * EPL + 64);
+  if (a.counts) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
+  float l[EPL], b[EPL], ahead[EPL];
+  auto fetch = [&](long t) {            // a token's logits, before its turn
+    const LT* row = (const LT*)a.logits + min(t, (long)a.T - 1) * a.stride;
+    if (a.vec) load_logits<EPL, true, LT>(row + e0, E - e0, ahead);
+    else load_logits<EPL, false, LT>(row + e0, E - e0, ahead);
+  };
+  const long turn = (long)gridDim.x * per_block;
+  const long t_first = (long)blockIdx.x * per_block + wv * SEGS + seg;
+  fetch(t_first);
+  if (a.bias) {                           // (a NaN reads as -inf: masked)
+    if (a.bias_vec) load_logits<EPL, true, float>(a.bias + e0, E - e0, b);
+    else load_logits<EPL, false, float>(a.bias + e0, E - e0, b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) b[i] = 0.0f;
+  }
+  // value i of the lane that holds expert e, for each lane's own e
+  auto of_expert = [&](const float* x, int e) {
+    float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = r * EPL + i;
-      l[i] = e < E ? logit_of<LT>(row[e]) : -__builtin_inf();
+      const float f = __shfl(x[i], base + e / EPL, 64);
+      v = e % EPL == i ? f : v;
     }
+    return v;
+  };
+  for (long t = t_first; __ballot(t < a.T); t += turn) {
+    const bool valid = t < a.T;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = ahead[i];
+    if (__ballot(t + turn < a.T)) fetch(t + turn);
+    // float32 choices and a bound on a score's error: the sigmoid's is 4 ulp
+    // of 1 at most (exponent's argument and the three operations), 2^-21
+    // taken; softmax scores are rounded from double
+    float c[EPL];
     double m = 0.0, sum = 0.0;
-    if (!a.sigmoid) {
-      m = l[0];
-#pragma unroll
-      for (int i = 1; i < EPL; ++i) m = fmax(m, l[i]);
-      m = seg_max<LANES>(m);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        c[i] = softmax_num(l[i], m);
-        sum += c[i];
-      }
-      sum = seg_sum<LANES>(sum);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = r * EPL + i;
-      double v = a.sigmoid ? sigmoid_f64(l[i]) : (sum > 0.0 ? c[i] / sum : 0.0);
-      if (a.bias) v += (double)a.bias[e < E ? e : 0];
-      // NaN compares false: a NaN bias masks too
-      c[i] = (l[i] > -__builtin_inf() && v > -__builtin_inf()) ? v : kMasked;
-      if (e >= E) c[i] = kGone;
-    }
-    if (a.groups > 1) {
-      double* ch = lds_c[wv][seg];
-      double* gs = lds_g[wv][seg];
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) ch[r * EPL + i] = c[i];
-      __syncthreads();
-      for (int g = r; g < a.groups; g += LANES) {
-        double b0 = kMasked, b1 = kMasked;     // the group's two best
-        for (int i = 0; i < a.per; ++i) {
-          const double v = ch[g * a.per + i];
-          b1 = fmax(b1, fmin(b0, v));
-          b0 = fmax(b0, v);
-        }
-        gs[g] = (a.group_top == 2 && b1 > kMasked) ? b0 + b1 : b0;
-      }
-      __syncthreads();
-      uint64_t stays = 0;                      // groups that stay
-      for (int g = r; g < a.groups; g += LANES) {
-        const double v = gs[g];
-        int better = 0;
-        for (int h = 0; h < a.groups; ++h)
-          better += (gs[h] > v || (gs[h] == v && h < g)) ? 1 : 0;
-        if (better < a.keep) stays |= 1ull << g;
-      }
-#pragma unroll
-      for (int s = 1; s < LANES; s <<= 1) {
-        const uint32_t lo = __shfl_xor((uint32_t)stays, s, 64);
-        const uint32_t hi = __shfl_xor((uint32_t)(stays >> 32), s, 64);
-        stays |= ((uint64_t)hi << 32) | lo;
-      }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const uint32_t g = ((uint32_t)(r * EPL + i) * a.per_inv) >> 20;
-        if (!((stays >> (g & 63)) & 1)) c[i] = kGone;
-      }
-      __syncthreads();                         // lds_c is written again
-    }
-    int my_id = 0;
-    for (int j = 0; j < k; ++j) {
-      double best = c[0];
-      int bi = 0;
-#pragma unroll
-      for (int i = 1; i < EPL; ++i)
-        if (c[i] > best) { best = c[i]; bi = i; }
-      const double top = seg_max<LANES>(best);
-      const int owner = seg_first<LANES>(best == top, base);
-      const int e = __shfl(r * EPL + bi, owner, 64);
-      if (r == j) my_id = e;
+    float err;
+    if (a.sigmoid) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (r * EPL + i == e) c[i] = kGone;
+        c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -1.44269504088896340736f));
+      err = 0x1p-21f;
+    } else {
+      float top = l[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) top = fmaxf(top, l[i]);
+      m = (double)seg_max<LANES>(top);
+      double p[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        p[i] = softmax_num((double)l[i], m);
+        sum += p[i];
+      }
+      sum = seg_sum<LANES>(sum);
+      const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = (float)(p[i] * inv);
+      err = 0x1p-23f;
     }
-    // lane j < k: the score of slot j again, from its logit
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = l[i] > -kInf ? c[i] + b[i] : -kInf;
+    bool sure = true;
+    uint32_t key[EPL], left;              // masked choices are -inf, the lowest
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = e0 + i < E ? order_of(c[i]) : 0u;
+    if (a.groups > 1) {
+      float gap, big;
+      stay_mask<LANES, EPL, float>(a, c, key, -kInf, r, base, scratch, &gap, &big);
+      // two sums of two choices each, with their own rounding
+      // (past 1e37 a float32 sum may overflow)
+      sure = gap > 4.0f * (err + big * 0x1p-22f) && big < 1e37f;
+    }
+    int my_id = take_slots<LANES, EPL>(key, k, r, base, &left);
+    const float next = from_order(max(seg_max<LANES>(left), order_of(-kInf)));
+    // lane j < k: the score and choice of slot j in double
     const bool slot = r < k;
-    const double lj = slot ? logit_of<LT>(row[my_id]) : -__builtin_inf();
-    double s = a.sigmoid ? sigmoid_f64(lj) : (sum > 0.0 ? softmax_num(lj, m) / sum : 0.0);
+    const double low = -__builtin_inf();
+    auto score_of = [&](double lj) {
+      return a.sigmoid ? sigmoid_f64(lj) : (sum > 0.0 ? softmax_num(lj, m) / sum : 0.0);
+    };
+    double lj = (double)of_expert(l, my_id);
+    if (!slot) lj = low;
+    double s = score_of(lj);
+    double v = low;
+    const float bj = a.bias ? of_expert(b, my_id) : 0.0f;
+    if (lj > low) v = s + (double)bj;
+    {
+      const double v1 = dpp<0x101>(v);                   // the next lane's
+      const int id1 = (int)dpp<0x101>((uint32_t)my_id);
+      if (r < k - 1 && v1 > low) sure = sure && (v > v1 || (v == v1 && my_id < id1));
+      if (r == k - 1 && next > -kInf)
+        sure = sure && v > (double)next + (double)(err + fabsf(next) * 0x1p-22f);
+    }
+    if (__ballot(!sure)) {
+      double c64[EPL];
+      uint64_t key64[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        c64[i] = score_of((double)l[i]) + (double)b[i];
+        if (!(c[i] > -kInf)) c64[i] = kMasked;
+        key64[i] = e0 + i < E ? key_of(c64[i]) : kGone;
+      }
+      if (a.groups > 1)
+        stay_mask<LANES, EPL, double>(a, c64, key64, kMasked, r, base, scratch, nullptr, nullptr);
+      uint64_t rest;
+      my_id = take_slots<LANES, EPL>(key64, k, r, base, &rest);
+      lj = (double)of_expert(l, my_id);
+      s = score_of(slot ? lj : low);
+    }
     if (a.renorm) {
-      const double S = seg_sum<LANES>(slot ? s : 0.0);
+      const double S = row_sum(slot ? s : 0.0);   // the slots' lanes are a row
       s = S > 0.0 ? s / S : 0.0;
     }
     if (valid && slot) {
       a.ids[t * k + r] = my_id;
       a.w[t * k + r] = (float)((double)a.scale * s);
+      if (a.counts) atomicAdd(&hist[my_id], 1);
     }
+  }
+  if (a.counts) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+      a.counts[(size_t)blockIdx.x * E + e] = hist[e];
   }
 }
 
+constexpr int kGradWaves = 4;
+
 template <int LANES, int EPL, typename LT>
-__global__ __launch_bounds__(64 * kWaves) void k_route_scored_backward(
+__global__ __launch_bounds__(64 * kGradWaves) void k_route_scored_backward(
     RouteArgs a, const int32_t* __restrict__ ids,
     const float* __restrict__ d_w, LT* __restrict__ d_logits) {
   constexpr int SEGS = 64 / LANES;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = lane & (LANES - 1), seg = lane / LANES, base = seg * LANES;
   const int E = a.E, k = a.k;
-  const int per_block = kWaves * SEGS;
+  const int per_block = kGradWaves * SEGS;
   // a softmax with renormalised weights is the softmax over the k chosen:
   // only their logits are read
   const bool dense = !a.sigmoid && !a.renorm;
@@ -248,7 +553,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_scored_backward(
       id = ids[t * k + r];
       if (id < 0 || id >= E) id = -1;
       if (id >= 0) {
-        lj = logit_of<LT>(row[id]);
+        lj = (double)logit_of(row[id]);
         dw = (double)a.scale * (double)d_w[t * k + r];
       }
     }
@@ -258,10 +563,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_scored_backward(
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = r * EPL + i;
-        p[i] = e < E ? logit_of<LT>(row[e]) : -__builtin_inf();
+        p[i] = e < E ? (double)logit_of(row[e]) : -__builtin_inf();
         m = fmax(m, p[i]);
       }
-      m = seg_max<LANES>(m);
+      m = (double)seg_max<LANES>((float)m);
       sum = 0.0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
@@ -270,7 +575,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_scored_backward(
       }
       sum = seg_sum<LANES>(sum);
     } else if (!a.sigmoid) {
-      m = seg_max<LANES>(lj);
+      m = (double)seg_max<LANES>((float)lj);
     }
     const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
     double s = a.sigmoid ? sigmoid_f64(lj) : softmax_num(lj, m) * inv;
@@ -315,39 +620,54 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_scored_backward(
   }
 }
 
-// Expert counts of a large batch: a workgroup counts its share of the ids in
-// LDS and stores its histogram; a second launch sums the histograms.
-constexpr int kCountIds = 4096;     // ids a workgroup counts
-
-__global__ __launch_bounds__(256) void k_count_share(
-    const int32_t* __restrict__ ids, long n, int E, int32_t* __restrict__ part) {
-  __shared__ int32_t h[4][MOE_EMAX];
-  const int tid = threadIdx.x;
-  for (int i = tid; i < 4 * E; i += 256) h[i / E][i % E] = 0;
-  __syncthreads();
-  const long b = (long)blockIdx.x * kCountIds;
-  const long end = b + kCountIds < n ? b + kCountIds : n;
-  for (long i = b + tid; i < end; i += 256) {
-    const int e = ids[i];
-    if ((unsigned)e < (unsigned)E) atomicAdd(&h[tid >> 6][e], 1);
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += 256)
-    part[(size_t)blockIdx.x * E + e] = h[0][e] + h[1][e] + h[2][e] + h[3][e];
-}
-
-__global__ __launch_bounds__(256) void k_count_sum(
+// counts[e] = sum of the workgroups' counts
+__global__ __launch_bounds__(1024) void k_count_sum(
     const int32_t* __restrict__ part, int parts, int E,
     int32_t* __restrict__ counts) {
-  __shared__ int32_t s[4][64];
+  __shared__ int32_t s[16][64];
   const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + c;
   int v = 0;
-  if (e < E)
-    for (int p = q; p < parts; p += 4) v += part[(size_t)p * E + e];
+  if (e < E) {
+#pragma unroll 8
+    for (int p = q; p < parts; p += 16) v += part[(size_t)p * E + e];
+  }
   s[q][c] = v;
   __syncthreads();
-  if (q == 0 && e < E) counts[e] = s[0][c] + s[1][c] + s[2][c] + s[3][c];
+  if (q == 0 && e < E) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) v += s[k][c];
+    counts[e] = v;
+  }
+}
+
+// Lanes a token's experts take, and experts a lane.  (256 experts on 16 lanes,
+// four tokens a wavefront, measured the same for 8192 tokens, 18 us, and 8.5
+// us instead of 5.1 for one.)
+int lanes_of(int E) { return E <= 64 ? 16 : 64; }
+int per_lane(int E, int lanes) {
+  int n = 1;
+  while (lanes * n < E) n *= 2;
+  return n;
+}
+
+// calls f(integral LANES, integral EPL)
+template <class F>
+void by_experts(int E, int lanes, F f) {
+  using std::integral_constant;
+  const int n = per_lane(E, lanes);
+  if (lanes == 16) {
+    integral_constant<int, 16> l;
+    if (n == 1) f(l, integral_constant<int, 1>{});
+    else if (n == 2) f(l, integral_constant<int, 2>{});
+    else f(l, integral_constant<int, 4>{});
+  } else {
+    integral_constant<int, 64> l;
+    if (n == 2) f(l, integral_constant<int, 2>{});
+    else if (n == 4) f(l, integral_constant<int, 4>{});
+    else if (n == 8) f(l, integral_constant<int, 8>{});
+    else f(l, integral_constant<int, 16>{});
+  }
 }
 
 RouteArgs route_args(const moe_router* r, const void* logits) {
@@ -363,36 +683,46 @@ RouteArgs route_args(const moe_router* r, const void* logits) {
   a.renorm = r->renormalize;
   a.per = r->E / r->groups;
   a.per_inv = ((1u << 20) + a.per - 1) / a.per;
+  const int n = per_lane(r->E, lanes_of(r->E));
+  if (a.groups > 1 && a.per % n == 0) {
+    const int lanes = a.per / n;
+    if (lanes <= 16 && (lanes & (lanes - 1)) == 0) a.spread = lanes;
+  }
+  const int bytes = r->logits_dtype == MOE_BF16 ? 2 : 4;
+  const int piece = n * bytes < 16 ? n * bytes : 16;
+  a.vec = (uintptr_t)logits % piece == 0 && r->logits_stride * bytes % piece == 0;
   a.scale = r->scale;
   a.stride = r->logits_stride;
   return a;
 }
 
-int route_grid(int T, int E) {
-  const int per_block = kWaves * (E <= 64 ? 4 : 1);
-  const long n = ((long)T + per_block - 1) / per_block;
-  return (int)(n < 65536 ? n : 65536);
-}
-
-// calls f(integral LANES, integral EPL)
-template <class F>
-void by_experts(int E, F f) {
-  using std::integral_constant;
-  if (E <= 16) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  else if (E <= 32) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  else if (E <= 64) f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-  else if (E <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  else if (E <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-  else if (E <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-  else f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+// Workgroups and wavefronts: a token's segment a wavefront's turn; the
+// wavefronts that stay on the GPU at once walk larger batches.
+struct RouteShape {
+  int waves, grid;
+};
+RouteShape route_shape(int T, int E) {
+  const int segs = 64 / lanes_of(E);
+  const long w = ((long)T + segs - 1) / segs;
+  RouteShape s;
+  s.waves = (int)(w < kWaves ? w : kWaves);
+  s.grid = (int)std::min<long>((w + s.waves - 1) / s.waves, 512);
+  return s;
 }
 
 }  // namespace
 
+// Expert counts: a single workgroup stores its own; some thousand ids are
+// counted again by one workgroup; beyond, every workgroup leaves its counts in
+// the scratch and a second launch sums them.
+static bool sums_counts(const moe_router* r, const RouteShape& s) {
+  return s.grid > 1 && (long)r->T * r->k > 8192;
+}
+
 size_t route_scored_partials(const moe_router* r) {
-  const long n = (long)r->T * r->k;
-  if (n <= 2 * kCountIds) return 0;
-  return (size_t)((n + kCountIds - 1) / kCountIds) * r->E;
+  if (r->T == 0) return 0;
+  const RouteShape s = route_shape(r->T, r->E);
+  return sums_counts(r, s) ? (size_t)s.grid * r->E : 0;
 }
 
 hipError_t launch_route_scored(const moe_router* r, const void* logits,
@@ -401,22 +731,26 @@ hipError_t launch_route_scored(const moe_router* r, const void* logits,
                                hipStream_t s) {
   RouteArgs a = route_args(r, logits);
   a.bias = bias;
+  a.bias_vec = (uintptr_t)bias % 16 == 0;
   a.ids = ids;
   a.w = w;
-  const dim3 grid(route_grid(r->T, r->E)), block(64 * kWaves);
-  by_experts(r->E, [&](auto lanes, auto epl) {
+  const RouteShape sh = route_shape(r->T, r->E);
+  const bool sum = counts && sums_counts(r, sh);
+  a.counts = sum ? partials : sh.grid == 1 ? counts : nullptr;
+  const dim3 grid(sh.grid), block(64 * sh.waves);
+  by_experts(r->E, lanes_of(r->E), [&](auto lanes, auto epl) {
+    constexpr int L = lanes.value, N = epl.value;
+    const size_t lds = a.groups > 1 && !a.spread
+                           ? sizeof(double) * sh.waves * (64 / L) * (L * N + 64) : 0;
     if (r->logits_dtype == MOE_F32)
-      k_route_scored<lanes.value, epl.value, float><<<grid, block, 0, s>>>(a);
+      k_route_scored<L, N, float><<<grid, block, lds, s>>>(a);
     else
-      k_route_scored<lanes.value, epl.value, bf16_t><<<grid, block, 0, s>>>(a);
+      k_route_scored<L, N, bf16_t><<<grid, block, lds, s>>>(a);
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !counts) return e;
-  const long n = (long)r->T * r->k;
-  if (n <= 2 * kCountIds) return launch_count_ids(ids, (int)n, r->E, counts, s);
-  const int parts = (int)((n + kCountIds - 1) / kCountIds);
-  k_count_share<<<parts, 256, 0, s>>>(ids, n, r->E, partials);
-  k_count_sum<<<(r->E + 63) / 64, 256, 0, s>>>(partials, parts, r->E, counts);
+  if (e != hipSuccess || !counts || sh.grid == 1) return e;
+  if (!sum) return launch_count_ids(ids, r->T * r->k, r->E, counts, s);
+  k_count_sum<<<(r->E + 63) / 64, 1024, 0, s>>>(partials, sh.grid, r->E, counts);
   return hipGetLastError();
 }
 
@@ -424,15 +758,16 @@ hipError_t launch_route_scored_backward(const moe_router* r,
                                         const void* logits,
                                         const int32_t* ids, const float* d_w,
                                         void* d_logits, hipStream_t s) {
-  const RouteArgs a = route_args(r, logits);
-  const dim3 grid(route_grid(r->T, r->E)), block(64 * kWaves);
-  by_experts(r->E, [&](auto lanes, auto epl) {
+  RouteArgs a = route_args(r, logits);
+  const int per_block = kGradWaves * (64 / lanes_of(r->E));
+  const dim3 grid((int)std::min<long>(((long)r->T + per_block - 1) / per_block, 65536));
+  const dim3 block(64 * kGradWaves);
+  by_experts(r->E, lanes_of(r->E), [&](auto lanes, auto epl) {
+    constexpr int L = lanes.value, N = epl.value;
     if (r->logits_dtype == MOE_F32)
-      k_route_scored_backward<lanes.value, epl.value, float>
-          <<<grid, block, 0, s>>>(a, ids, d_w, (float*)d_logits);
+      k_route_scored_backward<L, N, float><<<grid, block, 0, s>>>(a, ids, d_w, (float*)d_logits);
     else
-      k_route_scored_backward<lanes.value, epl.value, bf16_t>
-          <<<grid, block, 0, s>>>(a, ids, d_w, (bf16_t*)d_logits);
+      k_route_scored_backward<L, N, bf16_t><<<grid, block, 0, s>>>(a, ids, d_w, (bf16_t*)d_logits);
   });
   return hipGetLastError();
 }
