@@ -449,23 +449,33 @@ def make_norm(T, H, block="bf16", resid="bf16", out="bf16", gain="f32",
 def _enqueue(name, first, stream, check, *args) -> int:
     """Call an entry point on ``stream``, or on the current stream of the
     device that holds ``first`` (with that device current)."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     if stream is not None:
         st = fn(*args, stream)
-    else:
-        dev = getattr(first, "device", None)
-        if dev is not None and dev.type == "cuda":
-            import torch
-            if dev.index != torch.cuda.current_device():
-                with torch.cuda.device(dev):
-                    st = fn(*args, current_stream())
-            else:
-                st = fn(*args, current_stream())
+    elif getattr(first, "is_cuda", False):
+        import torch
+        dev = first.device.index
+        if dev == torch.cuda.current_device():
+            st = fn(*args, _raw_stream(dev))
         else:
-            st = fn(*args, current_stream())
-    if check:
-        _check(st, name)
+            with torch.cuda.device(dev):
+                st = fn(*args, _raw_stream(dev))
+    else:
+        st = fn(*args, current_stream())
+    if check and st != MOE_OK:
+        raise MoeError(st, name)
     return st
+
+
+def _raw_stream(device: int) -> int:
+    """hipStream_t of a device's current stream.  torch's Stream objects cost
+    3 us a call to make, more than everything else a call does before its
+    launch, so the handle is read without one where torch offers that."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(device)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def moe_check_router(r: Router) -> int:
