@@ -670,6 +670,9 @@ static moe_status check_norm_forward(const moe_norm* n, const NormArgs& a) {
   if ((a.pre_gain != nullptr) != (a.x_out != nullptr))
     return MOE_ERR_INVALID_ARGUMENT;
   if (a.gate && !gate_shape_ok(n)) return MOE_ERR_INVALID_ARGUMENT;
+  // in place: the same rows
+  if (a.resid_out == a.resid && n->resid_out_stride != n->resid_stride)
+    return MOE_ERR_INVALID_ARGUMENT;
   return MOE_OK;
 }
 
@@ -710,6 +713,9 @@ moe_status moe_residual_norm_backward(
     if (!y && (post_gain || gate)) return MOE_ERR_INVALID_ARGUMENT;
     if ((pre_gain != nullptr) != (d_x != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
     if (pre_gain ? !resid_out : !d_resid_out) return MOE_ERR_INVALID_ARGUMENT;
+    if (d_resid && d_resid == d_resid_out &&
+        n->resid_out_stride != n->resid_stride)
+      return MOE_ERR_INVALID_ARGUMENT;
     if (!d_y && !d_resid && !d_post_gain && !d_gate && !d_pre_gain)
       return MOE_ERR_INVALID_ARGUMENT;
     const size_t need = norm_grad_partials(n) * sizeof(float);

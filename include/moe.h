@@ -38,7 +38,11 @@
  *    an id outside [0, E) is neither counted nor local (its pair_row is -1),
  *    and a map entry outside [0, P) drops its pair (pair_row -1).
  *  - T = 0 is valid: the call enqueues nothing and succeeds (an idle rank's
- *    dummy forward, infra-guide page, section 4.3).
+ *    dummy forward, infra-guide page, section 4.3), apart from the sums over
+ *    the tokens that some calls clear.
+ *  - The current device is the one of `stream` and of the arrays.  A workspace
+ *    serves one call at a time: calls that may overlap, on two streams or in
+ *    two captured graphs, have one each.
  *  - Re-entrant; no global mutable state, except the per-device scratch of
  *    moe_layer_forward_noalloc (see there).
  */
@@ -379,7 +383,8 @@ MOE_API moe_status moe_check_norm(const moe_norm* n);
  *   resid     [T][resid_stride]
  *   post_gain [H] or NULL;  gate see moe_norm, or NULL;
  *   pre_gain  [H], or NULL together with x_out (no norm before a next block)
- *   resid_out [T][resid_out_stride] out, or NULL; may be resid itself
+ *   resid_out [T][resid_out_stride] out, or NULL; may be resid itself (with
+ *             its stride)
  *   x_out     [T][out_stride] out
  * At least one output is given; outputs overlap no input otherwise. */
 MOE_API moe_status moe_residual_norm(const moe_norm* n, const void* y,
@@ -405,6 +410,7 @@ MOE_API moe_status moe_residual_norm_workspace_size(const moe_norm* n,
  *   d_resid_out [T][resid_out_stride] or NULL (zero)
  *   d_y         [T][block_stride] out, or NULL
  *   d_resid     [T][resid_stride] out, or NULL; may be d_resid_out itself
+ *               (with its stride)
  *   d_post_gain, d_pre_gain [H] float32 out, or NULL
  *   d_gate      float32 out in the gate's shape, or NULL
  * An output whose operand is absent is NULL.  T = 0 clears the gains' and the

@@ -140,6 +140,12 @@ def test_norm_arguments():
         assert forward(norm(gate_shape=shape), gate=P) == BAD
 
 
+def test_norm_in_place_needs_one_stride():
+    n = norm(resid_stride=300)
+    assert forward(n, ro=P) == BAD
+    assert backward(n, d_ro=P, d_r=P) == BAD
+
+
 def backward(n, y=P, ro=P, post=P, gate=None, pre=P, d_x=P, d_ro=P, d_y=P,
              d_r=P, d_post=P, d_gate=None, d_pre=P, ws=P, size=1 << 30):
     return m.moe_residual_norm_backward(

@@ -123,6 +123,29 @@ def test_masked_experts_and_rows(score, E, G, keep, k):
         check_route(logits, b, k, renormalize=False, **kw)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep", [(256, 8, 4), (64, 1, 1), (120, 6, 3)])
+def test_choices_closer_than_float32_resolves(score, E, G, keep):
+    """Equal logits told apart by biases some 1e-9 apart, and distinct logits
+    whose choices a bias brings together: the order is that of 64 bits."""
+    import torch
+    g = torch.Generator().manual_seed(8)
+    logits = make_logits(300, E, "f32", 14, ties=True)
+    bias = 1e-9 * torch.randn(E, generator=g)
+    # rows of one value but for steps of an ulp or so
+    logits[::3] = 1.0 + 2.0 ** -23 * torch.randint(0, 4, (100, E), generator=g)
+    logits, bias = logits.cuda(), bias.cuda()
+    for b in (bias, None):
+        check_route(logits, b, 8, score=score, groups=G, topk_groups=keep,
+                    group_top=2)
+    # choices all within 1e-7: the bias undoes the scores of one row
+    row = logits[1:2].expand(64, E).contiguous()
+    s = ob.scores(to_f64(row), score)[0]
+    undo = torch.from_numpy((0.5 - s).astype(np.float32)).cuda()
+    check_route(row, undo, 8, score=score, groups=G, topk_groups=keep,
+                group_top=2)
+
+
 def test_sliced_logits():
     """Rows of a wider array, from a base that is not 16-byte aligned."""
     for dtype in ("f32", "bf16"):
