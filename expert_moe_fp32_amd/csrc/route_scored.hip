@@ -642,23 +642,27 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_scored_backward(
   }
 }
 
-// counts[e] = sum of the workgroups' counts
+// counts[e] = sum of the workgroups' counts: 16 experts a workgroup, 64 slices
+// of the parts, four of them a wavefront
 __global__ __launch_bounds__(1024) void k_count_sum(
     const int32_t* __restrict__ part, int parts, int E,
     int32_t* __restrict__ counts) {
-  __shared__ int32_t s[16][64];
-  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + c;
+  __shared__ int32_t s[16][16];
+  const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int e = blockIdx.x * 16 + c;
   int v = 0;
   if (e < E) {
 #pragma unroll 8
-    for (int p = q; p < parts; p += 16) v += part[(size_t)p * E + e];
+    for (int p = q; p < parts; p += 64) v += part[(size_t)p * E + e];
   }
-  s[q][c] = v;
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if ((threadIdx.x & 63) < 16) s[threadIdx.x >> 6][c] = v;
   __syncthreads();
-  if (q == 0 && e < E) {
+  if (threadIdx.x < 16 && e < E) {
+    v = 0;
 #pragma unroll
-    for (int k = 1; k < 16; ++k) v += s[k][c];
+    for (int k = 0; k < 16; ++k) v += s[k][c];
     counts[e] = v;
   }
 }
@@ -772,7 +776,7 @@ hipError_t launch_route_scored(const moe_router* r, const void* logits,
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !counts || sh.grid == 1) return e;
   if (!sum) return launch_count_ids(ids, r->T * r->k, r->E, counts, s);
-  k_count_sum<<<(r->E + 63) / 64, 1024, 0, s>>>(partials, sh.grid, r->E, counts);
+  k_count_sum<<<(r->E + 15) / 16, 1024, 0, s>>>(partials, sh.grid, r->E, counts);
   return hipGetLastError();
 }
 
