@@ -307,13 +307,15 @@ __device__ __forceinline__ void sort_keys(K* key, uint32_t* id) {
   for (int n = EPL - 1; n > 0; --n) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const bool up = key[i + 1] > key[i];
-      const K hk = up ? key[i + 1] : key[i], lk = up ? key[i] : key[i + 1];
-      const uint32_t hi = up ? id[i + 1] : id[i], li = up ? id[i] : id[i + 1];
-      key[i] = hk;
-      key[i + 1] = lk;
-      id[i] = hi;
-      id[i + 1] = li;
+      // (values, not elements: a conditional between two elements of an array
+      // is an element, and its index would be chosen at run time)
+      const K a = key[i], b = key[i + 1];
+      const uint32_t ia = id[i], ib = id[i + 1];
+      const bool up = b > a;
+      key[i] = up ? b : a;
+      key[i + 1] = up ? a : b;
+      id[i] = up ? ib : ia;
+      id[i + 1] = up ? ia : ib;
     }
   }
 }
@@ -351,8 +353,9 @@ __device__ __forceinline__ int take_slots(K* key, int k, int r, int base, K* lef
     if constexpr (!kSort) {
 #pragma unroll
       for (int i = 1; i < EPL; ++i) {
-        const bool up = key[i] > head;
-        head = up ? key[i] : head;
+        const K a = key[i];
+        const bool up = a > head;
+        head = up ? a : head;
         head_id = up ? r * EPL + i : head_id;
       }
     }
@@ -374,10 +377,13 @@ __device__ __forceinline__ int take_slots(K* key, int k, int r, int base, K* lef
       const bool mine = (int)(threadIdx.x & 63) == owner;
 #pragma unroll
       for (int i = 0; i + 1 < EPL; ++i) {
-        key[i] = mine ? key[i + 1] : key[i];
-        id[i] = mine ? id[i + 1] : id[i];
+        const K a = key[i], b = key[i + 1];
+        const uint32_t ia = id[i], ib = id[i + 1];
+        key[i] = mine ? b : a;
+        id[i] = mine ? ib : ia;
       }
-      key[EPL - 1] = mine ? K(0) : key[EPL - 1];
+      const K a = key[EPL - 1];
+      key[EPL - 1] = mine ? K(0) : a;
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) key[i] = r * EPL + i == e ? K(0) : key[i];
