@@ -10,7 +10,9 @@
 // mean y^2, the second mean(q y) and the gate's row sum.  Gradients of gains
 // and of a gate along the columns add up in registers over a workgroup's
 // rows; a second launch sums the workgroups' rows in a fixed order.  Bound by
-// HBM: four rows in, two out.
+// HBM, four rows in and two out, and by the one workgroup of a long row that a
+// CU's registers hold: 4096 x 7168 bf16 with all operands 72 us = 4.9 TB/s,
+// and 5 us for the column sums (16 slices a column; 4 took 40 us).
 #include <algorithm>
 #include <type_traits>
 
