@@ -3,8 +3,8 @@
 // A workgroup holds its token's d_out row in registers, walks the token's
 // local slots, and for each reads the expert row once for the weight's
 // gradient and writes the row's gradient.  Bound by HBM, per local row H * 4
-// bytes in and out: 4096 x 7168, 32 of 256 experts here and a shared one, 85
-// us = 4.8 TB/s (one piece of four columns at a time and sums through LDS: 98
+// bytes in and out: 4096 x 7168, 32 of 256 experts here and a shared one, 79
+// us = 5.2 TB/s (one piece of four columns at a time and sums through LDS: 98
 // us).
 #include <type_traits>
 
@@ -15,22 +15,25 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPieces = 4;                     // pieces of 4 columns a thread
-constexpr int kCols = 4 * kThreads * kPieces;  // columns of one pass
+// A thread takes two pieces of four columns a pass and a workgroup as many
+// threads as the row needs, up to 1024 (4096 x 7168: 79 us; 256 threads with
+// four pieces and two passes 85 us, 512 with four pieces 80 us).
+constexpr int kPieces = 2;
+constexpr int kMostThreads = 1024;
 
 // Every wavefront holds the token's slots in its lanes, so the walk over the
 // local ones needs no exchange.  A pass's pieces of d_out and of a slot's row
 // are requested together; rows are read and written once, past the caches in
 // a batch that does not fit them (STREAM).
 template <typename T, bool STREAM>
-__global__ __launch_bounds__(kThreads) void k_combine_backward(
+__global__ __launch_bounds__(kMostThreads) void k_combine_backward(
     const T* __restrict__ d_out, const float* __restrict__ y_perm,
     const int32_t* __restrict__ pair_row, const float* __restrict__ w, int T_,
     int H, int k, int cap, float* __restrict__ d_y_perm,
     float* __restrict__ d_w, float* __restrict__ d_y_shared) {
-  __shared__ float part[2][4][MOE_KMAX];       // by token parity
+  __shared__ float part[2][kMostThreads / 64][MOE_KMAX];   // by token parity
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int NT = blockDim.x, waves = NT >> 6;
   int par = 0;
   for (long t = blockIdx.x; t < T_; t += gridDim.x, par ^= 1) {
     int row = -1;
@@ -41,12 +44,12 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
       if (row >= cap) row = -1;
     }
     float sums = 0.0f;                         // lane j: slot j, this wavefront's columns
-    for (int c0 = 0; c0 < H; c0 += kCols) {
+    for (int c0 = 0; c0 < H; c0 += 4 * kPieces * NT) {
       Piece pc[kPieces];
       f32x4_t d[kPieces];
 #pragma unroll
       for (int v = 0; v < kPieces; ++v) {
-        pc[v] = piece_at<4, kAligned>(c0 + 4 * (threadIdx.x + v * kThreads), H);
+        pc[v] = piece_at<4, kAligned>(c0 + 4 * (threadIdx.x + v * NT), H);
         d[v] = widen<T, 4>(own_cols<T, 4, kAligned>(
             load_piece<T, 4, kAligned, STREAM>(d_out + t * H, pc[v], H), pc[v]));
       }
@@ -83,9 +86,11 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
     if (d_w) {
       if (lane < k) part[par][wv][lane] = sums;
       lds_barrier();
-      if (threadIdx.x < k)
-        d_w[t * k + lane] = (part[par][0][lane] + part[par][1][lane]) +
-                            (part[par][2][lane] + part[par][3][lane]);
+      if (threadIdx.x < k) {
+        float s = part[par][0][lane];
+        for (int v = 1; v < waves; ++v) s += part[par][v][lane];
+        d_w[t * k + lane] = s;
+      }
     }
   }
 }
@@ -99,11 +104,13 @@ hipError_t launch_combine_backward(const void* d_out, int out_dtype,
                                    float* d_y_perm, float* d_w,
                                    float* d_y_shared, hipStream_t s) {
   const dim3 grid(T < (1 << 20) ? T : (1 << 20));
+  const int nt = (H + 4 * kPieces - 1) / (4 * kPieces);
+  const dim3 block(nt < kMostThreads ? (nt + 63) / 64 * 64 : kMostThreads);
   const bool stream = (double)T * H * 8 >= 64.0 * 1048576.0;
   by_type(out_dtype, [&](auto type) {
     using D = decltype(type);
     by_flag(stream, [&](auto st) {
-      k_combine_backward<D, st.value><<<grid, kThreads, 0, s>>>(
+      k_combine_backward<D, st.value><<<grid, block, 0, s>>>(
           (const D*)d_out, y_perm, pair_row, w, T, H, k, cap, d_y_perm, d_w,
           d_y_shared);
     });
