@@ -51,6 +51,8 @@ def combine_inputs(T, H, k, shared, seed, local=0.4):
     dict(T=11, H=16384, k=3, shared=True, resid="f32", gain="bf16", offset=1.0),
     dict(T=33, H=640, k=5, shared=False, pre=False, gate="full", rscale=0.5),
     dict(T=33, H=640, k=5, shared=True, pads=(1, 3, 5, 7)),
+    dict(T=530, H=8192, k=8, shared=False, resid="f32"),
+    dict(T=20, H=4, k=2, shared=True, block="f32"),
 ], ids=str)
 def test_combine_norm(kw):
     import torch
@@ -93,7 +95,8 @@ def test_combine_norm(kw):
     (1, 7168, 8, True, "bf16"), (50, 256, 2, False, "f32"),
     (133, 1024, 16, True, "f32"), (20, 36, 3, True, "bf16"),
     (9, 4, 2, False, "f32"), (7, 20480, 4, True, "bf16"),
-    (300, 6144, 8, False, "bf16"),
+    (300, 6144, 8, False, "bf16"), (1500, 7168, 2, True, "bf16"),
+    (3, 8196, 5, True, "f32"),
 ])
 def test_combine_backward(T, H, k, shared, out):
     import torch

@@ -24,6 +24,12 @@ CASES = [
     dict(T=1031, H=136, gate="channel"), dict(T=1031, H=24, gate="scalar"),
     dict(T=2, H=512, eps=0.0),
     dict(T=40, H=768, pre=False), dict(T=40, H=768, y=False, post=False),
+    dict(T=1, H=2), dict(T=5, H=3, block="f32", resid="f32", out="f32"),
+    dict(T=33, H=16384, gate="channel"), dict(T=300, H=12288, out="f32"),
+    dict(T=270, H=4096, gate="token"), dict(T=20, H=7168, post=False),
+    dict(T=600, H=2048, block="f32", resid="f32", out="f32", gate="channel"),
+    dict(T=1031, H=512, gate="full"), dict(T=1031, H=512, gate="scalar"),
+    dict(T=530, H=8192, resid="f32", gate="channel", rscale=-0.5),
 ]
 
 
