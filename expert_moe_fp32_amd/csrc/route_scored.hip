@@ -157,8 +157,8 @@ struct RouteArgs {
   const float* bias;
   int T, E, k, sigmoid, groups, keep, group_top, renorm, per;
   int vec, bias_vec;      // logits / bias rows load as vectors
-  int spread;             // lanes a group, when groups are runs of whole
-                          // lanes, 2^n of them up to 16; else 0
+  int whole;              // groups are runs of whole lanes, 2^share of them
+  int share;              // 2^share lanes find a group's best, share <= 4
   uint32_t per_inv;       // e / per == (e * per_inv) >> 20 for e < 1024
   float scale;
   int64_t stride;
@@ -208,8 +208,11 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Clears the keys of the experts whose group does not stay; V: float or double.  Groups of whole lanes by mirrored lanes,
-// others through `scratch` (LANES * EPL + 64 values of one token).
+// Clears the keys of the experts whose group does not stay; V: float or
+// double.  A group's two best choices are found by a run of neighbouring
+// lanes: those that hold its experts, where groups are whole lanes, else as
+// many as the segment has for a group, through `scratch` (LANES * EPL values
+// of one token).
 // For float *gap is the distance of the last group that stays from the best
 // that does not, and *big the largest choice's magnitude; gap = +inf where
 // the border lies at groups without a live expert.
@@ -219,84 +222,57 @@ __device__ __forceinline__ void stay_mask(const RouteArgs& a, const V* c, K* key
                                           double* scratch, float* gap,
                                           float* big) {
   const int e0 = r * EPL;
-  V score;
-  bool stays;
-  if (a.spread) {
-    V b0 = masked, b1 = masked;                 // the group's two best
+  const int sh = a.share, g = r >> sh;
+  V b0 = masked, b1 = masked;
+  if (a.whole) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       b1 = max_of(b1, min_of(b0, c[i]));
       b0 = max_of(b0, c[i]);
     }
-    if (a.spread >= 2) merge_best<0xB1>(b0, b1);     // lanes 1 0 3 2
-    if (a.spread >= 4) merge_best<0x4E>(b0, b1);     // lanes 2 3 0 1
-    if (a.spread >= 8) merge_best<0x141>(b0, b1);    // half row mirrored
-    if (a.spread >= 16) merge_best<0x140>(b0, b1);   // row mirrored
-    score = (a.group_top == 2 && b1 > masked) ? b0 + b1 : b0;
-    const int g = r / a.spread;
-    stays = group_stays(g, score, a.groups, a.keep, [&](int h) {
-      if (LANES == 64) return read_lane(score, h * a.spread);
-      return (V)__shfl(score, base + h * a.spread, 64);
-    });
+  } else {
+    V* ch = (V*)scratch;
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) ch[e0 + i] = c[i];
+    wave_fence();
+    if (g < a.groups) {
+#pragma unroll 4
+      for (int i = r - (g << sh); i < a.per; i += 1 << sh) {
+        const V v = ch[g * a.per + i];
+        b1 = max_of(b1, min_of(b0, v));
+        b0 = max_of(b0, v);
+      }
+    }
+  }
+  if (sh >= 1) merge_best<0xB1>(b0, b1);     // lanes 1 0 3 2
+  if (sh >= 2) merge_best<0x4E>(b0, b1);     // lanes 2 3 0 1
+  if (sh >= 3) merge_best<0x141>(b0, b1);    // half row mirrored
+  if (sh >= 4) merge_best<0x140>(b0, b1);   // row mirrored
+  V score = (a.group_top == 2 && b1 > masked) ? b0 + b1 : b0;
+  const bool stays = group_stays(g, score, a.groups, a.keep, [&](int h) {
+    if (LANES == 64) return read_lane(score, h << sh);
+    return (V)__shfl(score, base + (h << sh), 64);
+  }) && g < a.groups;
+  if (gap) {
     if (g >= a.groups) score = masked;
+    const float s32 = score > masked ? (float)score : -__builtin_inff();
+    const float low = seg_max<LANES>(stays && score > masked ? -s32 : -__builtin_inff());
+    const float next = seg_max<LANES>(stays ? -__builtin_inff() : s32);
+    *gap = next == -__builtin_inff() ? __builtin_inff() : -low - next;
+    *big = seg_max<LANES>(fmaxf(b0 > masked ? fabsf((float)b0) : 0.0f,
+                                b1 > masked ? fabsf((float)b1) : 0.0f));
+  }
+  if (a.whole) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = stays ? key[i] : K(0);
-    if (gap) *big = fmaxf(b0 > masked ? fabsf((float)b0) : 0.0f, b1 > masked ? fabsf((float)b1) : 0.0f);
-    if (gap) {
-      const float s32 = score > masked ? (float)score : -__builtin_inff();
-      const float low = seg_max<LANES>(stays && score > masked ? -s32 : -__builtin_inff());
-      const float next = seg_max<LANES>(stays ? -__builtin_inff() : s32);
-      *gap = next == -__builtin_inff() ? __builtin_inff() : -low - next;
-      *big = seg_max<LANES>(*big);
-    }
-    return;
-  }
-  V* ch = (V*)scratch;
-  V* gs = ch + LANES * EPL;
-  wave_fence();
+  } else {
+    const uint64_t kept = __ballot(stays) >> base;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) ch[e0 + i] = c[i];
-  wave_fence();
-  float most = 0.0f;
-  for (int g = r; g < a.groups; g += LANES) {
-    V b0 = masked, b1 = masked;
-    for (int i = 0; i < a.per; ++i) {
-      const V v = ch[g * a.per + i];
-      b1 = max_of(b1, min_of(b0, v));
-      b0 = max_of(b0, v);
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t h = ((uint32_t)(e0 + i) * a.per_inv) >> 20;
+      if (!((kept >> ((h << sh) & 63)) & 1)) key[i] = K(0);
     }
-    gs[g] = (a.group_top == 2 && b1 > masked) ? b0 + b1 : b0;
-    if (b0 > masked) most = fmaxf(most, fabsf((float)b0));
-    if (b1 > masked) most = fmaxf(most, fabsf((float)b1));
-  }
-  wave_fence();
-  uint64_t kept = 0;
-  float low = -__builtin_inff(), next = -__builtin_inff();
-  for (int g = r; g < a.groups; g += LANES) {
-    const V v = gs[g];
-    const bool in = group_stays(g, v, a.groups, a.keep, [&](int h) { return gs[h]; });
-    if (in) kept |= 1ull << g;
-    if (v > masked) {
-      if (in) low = fmaxf(low, -(float)v);
-      else next = fmaxf(next, (float)v);
-    }
-  }
-#pragma unroll
-  for (int s = 1; s < LANES; s <<= 1) {
-    const uint32_t lo = __shfl_xor((uint32_t)kept, s, 64);
-    const uint32_t hi = __shfl_xor((uint32_t)(kept >> 32), s, 64);
-    kept |= ((uint64_t)hi << 32) | lo;
-  }
-  if (gap) {
-    low = seg_max<LANES>(low);
-    next = seg_max<LANES>(next);
-    *gap = next == -__builtin_inff() ? __builtin_inff() : -low - next;
-    *big = seg_max<LANES>(most);
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const uint32_t g = ((uint32_t)(e0 + i) * a.per_inv) >> 20;
-    if (!((kept >> (g & 63)) & 1)) key[i] = K(0);
   }
 }
 
@@ -403,7 +379,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_scored(RouteArgs a) {
   const int r = lane & (LANES - 1), seg = lane / LANES, base = seg * LANES;
   const int E = a.E, k = a.k, e0 = r * EPL;
   const int waves = blockDim.x >> 6, per_block = waves * SEGS;
-  double* scratch = lds_groups + (wv * SEGS + seg) * (LANES * EPL + 64);
+  double* scratch = lds_groups + (wv * SEGS + seg) * (LANES * EPL);
   if (a.counts) {
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
@@ -677,7 +653,9 @@ __global__ __launch_bounds__(1024) void k_count_sum(
 // Lanes a token's experts take, and experts a lane.  (256 experts on 16 lanes,
 // four tokens a wavefront, measured the same for 8192 tokens, 18 us, and 8.5
 // us instead of 5.1 for one.)
-int lanes_of(int E) { return E <= 64 ? 16 : 64; }
+int lanes_of(const moe_router* r) {
+  return r->E <= 64 && r->groups <= 16 ? 16 : 64;
+}
 int per_lane(int E, int lanes) {
   int n = 1;
   while (lanes * n < E) n *= 2;
@@ -696,7 +674,8 @@ void by_experts(int E, int lanes, F f) {
     else f(l, integral_constant<int, 4>{});
   } else {
     integral_constant<int, 64> l;
-    if (n == 2) f(l, integral_constant<int, 2>{});
+    if (n == 1) f(l, integral_constant<int, 1>{});
+    else if (n == 2) f(l, integral_constant<int, 2>{});
     else if (n == 4) f(l, integral_constant<int, 4>{});
     else if (n == 8) f(l, integral_constant<int, 8>{});
     else f(l, integral_constant<int, 16>{});
@@ -716,10 +695,13 @@ RouteArgs route_args(const moe_router* r, const void* logits) {
   a.renorm = r->renormalize;
   a.per = r->E / r->groups;
   a.per_inv = ((1u << 20) + a.per - 1) / a.per;
-  const int n = per_lane(r->E, lanes_of(r->E));
-  if (a.groups > 1 && a.per % n == 0) {
+  const int all = lanes_of(r), n = per_lane(r->E, all);
+  if (a.groups > 1) {
     const int lanes = a.per / n;
-    if (lanes <= 16 && (lanes & (lanes - 1)) == 0) a.spread = lanes;
+    a.whole = a.per % n == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
+    while (a.share < 4 && (a.whole ? (1 << a.share) < lanes
+                                   : (2 << a.share) * a.groups <= all))
+      ++a.share;
   }
   const int bytes = r->logits_dtype == MOE_BF16 ? 2 : 4;
   const int piece = n * bytes < 16 ? n * bytes : 16;
@@ -734,9 +716,9 @@ RouteArgs route_args(const moe_router* r, const void* logits) {
 struct RouteShape {
   int waves, grid;
 };
-RouteShape route_shape(int T, int E) {
-  const int segs = 64 / lanes_of(E);
-  const long w = ((long)T + segs - 1) / segs;
+RouteShape route_shape(const moe_router* r) {
+  const int segs = 64 / lanes_of(r);
+  const long w = ((long)r->T + segs - 1) / segs;
   RouteShape s;
   s.waves = (int)(w < kWaves ? w : kWaves);
   s.grid = (int)std::min<long>((w + s.waves - 1) / s.waves, 512);
@@ -754,7 +736,7 @@ static bool sums_counts(const moe_router* r, const RouteShape& s) {
 
 size_t route_scored_partials(const moe_router* r) {
   if (r->T == 0) return 0;
-  const RouteShape s = route_shape(r->T, r->E);
+  const RouteShape s = route_shape(r);
   return sums_counts(r, s) ? (size_t)s.grid * r->E : 0;
 }
 
@@ -767,14 +749,14 @@ hipError_t launch_route_scored(const moe_router* r, const void* logits,
   a.bias_vec = (uintptr_t)bias % 16 == 0;
   a.ids = ids;
   a.w = w;
-  const RouteShape sh = route_shape(r->T, r->E);
+  const RouteShape sh = route_shape(r);
   const bool sum = counts && sums_counts(r, sh);
   a.counts = sum ? partials : sh.grid == 1 ? counts : nullptr;
   const dim3 grid(sh.grid), block(64 * sh.waves);
-  by_experts(r->E, lanes_of(r->E), [&](auto lanes, auto epl) {
+  by_experts(r->E, lanes_of(r), [&](auto lanes, auto epl) {
     constexpr int L = lanes.value, N = epl.value;
-    const size_t lds = a.groups > 1 && !a.spread
-                           ? sizeof(double) * sh.waves * (64 / L) * (L * N + 64) : 0;
+    const size_t lds = a.groups > 1 && !a.whole
+                           ? sizeof(double) * sh.waves * 64 * N : 0;
     if (r->logits_dtype == MOE_F32)
       k_route_scored<L, N, float><<<grid, block, lds, s>>>(a);
     else
@@ -793,10 +775,10 @@ hipError_t launch_route_scored_backward(const moe_router* r,
                                         void* d_logits, hipStream_t s) {
   RouteArgs a = route_args(r, logits);
   a.vec = a.vec && route_args(r, d_logits).vec;
-  const int per_block = kGradWaves * (64 / lanes_of(r->E));
+  const int per_block = kGradWaves * (64 / lanes_of(r));
   const dim3 grid((int)std::min<long>(((long)r->T + per_block - 1) / per_block, 65536));
   const dim3 block(64 * kGradWaves);
-  by_experts(r->E, lanes_of(r->E), [&](auto lanes, auto epl) {
+  by_experts(r->E, lanes_of(r), [&](auto lanes, auto epl) {
     constexpr int L = lanes.value, N = epl.value;
     if (r->logits_dtype == MOE_F32)
       k_route_scored_backward<L, N, float><<<grid, block, 0, s>>>(a, ids, d_w, (float*)d_logits);
