@@ -18,7 +18,7 @@
 // choices; a slot is then one max over the lanes' first keys in DPP steps of
 // one instruction, and the owner moves its list up.  Bound by instructions
 // (8192 tokens of 256 experts in 8 groups: 698 a token, 14 us; in double
-// throughout 1020, 20 us) and, for a single token, by their latency (4.6 us).
+// throughout 21 us) and, for a single token, by their latency (4.6 us).
 #include <float.h>
 #include <algorithm>
 #include <type_traits>
@@ -415,9 +415,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_scored(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) l[i] = ahead[i];
     if (__ballot(t + turn < a.T)) fetch(t + turn);
-    // float32 choices and a bound on a score's error: the sigmoid's is 4 ulp
-    // of 1 at most (exponent's argument and the three operations), 2^-21
-    // taken; softmax scores are rounded from double
+    // float32 choices and a bound on a score's error.  Sigmoid, in 2^-24: the
+    // exponent's argument s (1 - s) |l| 1.5 <= 0.34, its power s (1 - s) 2 <=
+    // 0.5, the sum 1, the reciprocal 2, together below 4 = 2^-22; twice that
+    // is taken.  Softmax scores are rounded from double.
     float c[EPL];
     double m = 0.0, sum = 0.0;
     float err;

@@ -256,3 +256,37 @@ def test_zero_tokens_enqueue_nothing():
                                stream=0, check=False) == L.MOE_OK
     assert m.moe_residual_norm_backward(
         n, *[None] * 12, None, 0, stream=0, check=False) == L.MOE_OK
+
+
+def test_calls_go_to_the_device_of_their_arrays(monkeypatch):
+    """Without a stream argument a call runs on the current stream of the
+    device that holds its arrays, with that device current."""
+    import contextlib
+
+    import torch
+
+    class OnDevice1:
+        is_cuda = True
+        device = torch.device("cuda", 1)
+
+        def data_ptr(self):
+            return P
+
+    seen = []
+
+    @contextlib.contextmanager
+    def device(d):
+        seen.append(("enter", d))
+        yield
+        seen.append(("leave", d))
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(L, "_raw_stream", lambda d: seen.append(("stream", d)) or 0)
+    a = OnDevice1()
+    m.moe_residual_norm(norm(T=0), a, a, None, None, a, a, a)
+    assert seen == [("enter", 1), ("stream", 1), ("leave", 1)]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    del seen[:]
+    m.moe_route_scored_backward(router(T=0), a, a, a, a)
+    assert seen == [("stream", 1)]
