@@ -189,13 +189,25 @@ class DeviceLayer:
             self.p, logits, bias, x, self.weights, self.l2p, self.rep, b.out,
             b.counts if counts else None, b.ws_layer, b.ws_layer.numel())
 
+    def _block_out(self, b: LayerBuffers, norm: Optional[L.Norm], out: bool,
+                   where: str):
+        """`b.out` for a call that ends in a norm: it holds contiguous rows of
+        the problem's out_dtype, so a norm of other block rows is refused
+        (`out=False` does without them)."""
+        if out and norm is not None and (
+                norm.block_dtype != self.p.out_dtype
+                or (norm.T > 1 and norm.block_stride != self.p.H)):
+            raise L.MoeError(L.MOE_ERR_INVALID_ARGUMENT, where)
+        return b.out if out else None
+
     def forward_scored(self, b: LayerBuffers, router: L.Router, logits, bias,
                        x, norm: Optional[L.Norm] = None, resid=None,
                        post_gain=None, gate=None, pre_gain=None,
                        resid_out=None, x_out=None, counts=True, out=True):
         return L.moe_layer_forward_scored(
             self.p, router, norm, logits, bias, x, self.weights, self.l2p,
-            self.rep, resid, post_gain, gate, pre_gain, b.out if out else None,
+            self.rep, resid, post_gain, gate, pre_gain,
+            self._block_out(b, norm, out, "forward_scored"),
             resid_out, x_out, b.counts if counts else None, b.ws_layer,
             b.ws_layer.numel())
 
@@ -228,8 +240,9 @@ class DeviceLayer:
                      gate, pre_gain, resid_out, x_out, out=True):
         return L.moe_combine_norm(self.p, norm, b.y_perm, b.pair_row, b.w,
                                   b.y_shared, resid, post_gain, gate,
-                                  pre_gain, b.out if out else None, resid_out,
-                                  x_out)
+                                  pre_gain,
+                                  self._block_out(b, norm, out, "combine_norm"),
+                                  resid_out, x_out)
 
     def combine_backward(self, b: LayerBuffers, d_out, d_y_perm, d_w,
                          d_y_shared=None):

@@ -290,3 +290,53 @@ def test_calls_go_to_the_device_of_their_arrays(monkeypatch):
     del seen[:]
     m.moe_route_scored_backward(router(T=0), a, a, a, a)
     assert seen == [("stream", 1)]
+
+
+def bare_layer(p):
+    """A DeviceLayer's calls without its weights or a device."""
+    from expert_moe_fp32_amd.runner import DeviceLayer
+    dl = object.__new__(DeviceLayer)
+    dl.p, dl.weights, dl.l2p, dl.rep = p, L.Weights(), None, None
+    return dl
+
+
+class Anything:
+    """Buffers that stand for addresses."""
+
+    def __getattr__(self, name):
+        return type("Buffer", (), {"numel": lambda s: 1 << 40,
+                                   "data_ptr": lambda s: P})()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(block="f32"),                           # rows twice as long
+    dict(block_stride=264),
+    dict(block="f32", block_stride=512),
+], ids=str)
+def test_layer_buffers_take_no_other_block_rows(monkeypatch, kw):
+    """A layer's `out` buffer holds T x H elements of the problem's out_dtype:
+    combined rows of another type or stride never go there."""
+    for name in ("moe_layer_forward_scored", "moe_combine_norm"):
+        monkeypatch.setattr(L, name, lambda *a, _n=name, **k: _n)
+    p, b = problem(out="bf16"), Anything()
+    dl, r = bare_layer(p), m.make_router(8, 16, 4)
+    n = norm(**kw)
+
+    def calls(n, **k):
+        return [lambda: dl.forward_scored(b, r, P, None, P, n, P, None, None,
+                                          P, P, P, **k),
+                lambda: dl.combine_norm(b, n, P, None, None, P, P, P, **k)]
+
+    for call in calls(n):
+        with pytest.raises(m.MoeError) as e:
+            call()
+        assert e.value.status == BAD
+    for call in calls(n, out=False) + calls(norm()):     # no rows, or fitting
+        assert call().startswith("moe_")
+    assert dl.forward_scored(b, r, P, None, P) == "moe_layer_forward_scored"
+    one = bare_layer(problem(T=1))               # a single row has no stride
+    assert one.combine_norm(b, norm(T=1, block_stride=264), P, None, None, P,
+                            P, P) == "moe_combine_norm"
+    f32 = bare_layer(problem(out="f32", act="f32", wdt="f32"))
+    with pytest.raises(m.MoeError):
+        f32.combine_norm(b, norm(), P, None, None, P, P, P)
