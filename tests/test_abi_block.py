@@ -340,3 +340,17 @@ def test_layer_buffers_take_no_other_block_rows(monkeypatch, kw):
     f32 = bare_layer(problem(out="f32", act="f32", wdt="f32"))
     with pytest.raises(m.MoeError):
         f32.combine_norm(b, norm(), P, None, None, P, P, P)
+
+
+@pytest.mark.parametrize("size", [(9, 16, 4), (8, 32, 4), (8, 16, 5),
+                                  (4, 16, 4)], ids=str)
+def test_layer_buffers_take_no_other_routing(monkeypatch, size):
+    """A layer's ids, weights and counts hold its problem's T, k and E."""
+    monkeypatch.setattr(L, "moe_route_scored", lambda *a, **k: "called")
+    dl = bare_layer(problem())
+    dl.device = "cpu"
+    with pytest.raises(m.MoeError) as e:
+        dl.route_scored(Anything(), m.make_router(*size), P, None)
+    assert e.value.status == BAD
+    assert dl.route_scored(Anything(), m.make_router(8, 16, 4), P,
+                           None) == "called"
