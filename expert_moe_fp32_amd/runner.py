@@ -213,7 +213,7 @@ class DeviceLayer:
 
     def route_scored(self, b: LayerBuffers, router: L.Router, logits, bias):
         p = self.p                     # (what the buffers were made for)
-        if (router.T, router.E, router.k) != (p.T, p.E, p.k):
+        if router.T * router.k > p.T * p.k or router.E > p.E:
             raise L.MoeError(L.MOE_ERR_INVALID_ARGUMENT, "route_scored")
         n = L.moe_route_scored_workspace_size(router)
         ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None

@@ -342,8 +342,8 @@ def test_layer_buffers_take_no_other_block_rows(monkeypatch, kw):
         f32.combine_norm(b, norm(), P, None, None, P, P, P)
 
 
-@pytest.mark.parametrize("size", [(9, 16, 4), (8, 32, 4), (8, 16, 5),
-                                  (4, 16, 4)], ids=str)
+@pytest.mark.parametrize("size", [(9, 16, 4), (8, 32, 4), (8, 16, 5)],
+                         ids=str)
 def test_layer_buffers_take_no_other_routing(monkeypatch, size):
     """A layer's ids, weights and counts hold its problem's T, k and E."""
     monkeypatch.setattr(L, "moe_route_scored", lambda *a, **k: "called")
@@ -352,5 +352,6 @@ def test_layer_buffers_take_no_other_routing(monkeypatch, size):
     with pytest.raises(m.MoeError) as e:
         dl.route_scored(Anything(), m.make_router(*size), P, None)
     assert e.value.status == BAD
-    assert dl.route_scored(Anything(), m.make_router(8, 16, 4), P,
-                           None) == "called"
+    for fits in ((8, 16, 4), (4, 16, 4), (8, 8, 4)):
+        assert dl.route_scored(Anything(), m.make_router(*fits), P,
+                               None) == "called"
