@@ -551,8 +551,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_scored_backward(
   const int E = a.E, k = a.k;
   const int per_block = kGradWaves * SEGS;
   double* parts = lds_row[wv][seg];
-  // a softmax with renormalised weights is the softmax over the k chosen:
-  // only their logits are read
+  // A softmax with renormalised weights is the softmax over the k chosen,
+  // unless their scores among all E vanish (a bias lifted experts far below
+  // the row's largest logit): the row is read for that alone, its sum only
+  // where it can be (8192 x 256: 7.8 us; the k logits alone 6.0).
   const bool dense = !a.sigmoid && !a.renorm;
   for (long t0 = (long)blockIdx.x * per_block; t0 < a.T;
        t0 += (long)gridDim.x * per_block) {
@@ -560,6 +562,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_scored_backward(
     const bool valid = tt < a.T;
     const long t = valid ? tt : a.T - 1;
     const LT* row = (const LT*)a.logits + t * a.stride;
+    float l[EPL];                      // requested ahead of the slots' chain
+    if (!a.sigmoid) {
+      if (a.vec) load_logits<EPL, true, LT>(row + r * EPL, E - r * EPL, l);
+      else load_logits<EPL, false, LT>(row + r * EPL, E - r * EPL, l);
+    }
     int id = -1;
     double lj = -__builtin_inf(), dw = 0.0;
     if (r < k) {
@@ -571,22 +578,28 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_scored_backward(
       }
     }
     double p[EPL], m = 0.0, sum = 1.0;
-    if (dense) {
-      float l[EPL], top = -__builtin_inff();
-      if (a.vec) load_logits<EPL, true, LT>(row + r * EPL, E - r * EPL, l);
-      else load_logits<EPL, false, LT>(row + r * EPL, E - r * EPL, l);
+    bool vanish = false;               // the chosen scores are all 0
+    if (!a.sigmoid) {
+      float top = l[0];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
-      m = (double)seg_max<LANES>(top);
-      sum = 0.0;
+      for (int i = 1; i < EPL; ++i) top = fmaxf(top, l[i]);
+      const float best = dense ? 0.0f : seg_max<LANES>((float)lj);
+      // (exp(-700) / 1024 is a normal number: nothing vanishes before)
+      if (dense || __ballot(top - best > 700.0f)) {
+        m = (double)seg_max<LANES>(top);
+        sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        p[i] = softmax_num((double)l[i], m);
-        sum += p[i];
+        for (int i = 0; i < EPL; ++i) {
+          p[i] = softmax_num((double)l[i], m);
+          sum += p[i];
+        }
+        sum = seg_sum<LANES>(sum);
+        if (!dense) vanish = !(softmax_num((double)best, m) / sum > 0.0);
       }
-      sum = seg_sum<LANES>(sum);
-    } else if (!a.sigmoid) {
-      m = (double)seg_max<LANES>((float)lj);
+      if (!dense) {
+        m = (double)best;
+        sum = 1.0;
+      }
     }
     const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
     double s = a.sigmoid ? sigmoid_f64(lj) : softmax_num(lj, m) * inv;
@@ -594,7 +607,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_scored_backward(
     if (a.renorm) {
       const double S = row_sum(s);     // (the slots' lanes are a row)
       const double q = row_sum(s > 0.0 ? dw * s : 0.0);
-      ds = S > 0.0 ? (dw - q / S) / S : 0.0;
+      ds = S > 0.0 && !vanish ? (dw - q / S) / S : 0.0;
     }
     // slot j's own part, and for a dense softmax the part of every expert
     double part = 0.0, all = 0.0;

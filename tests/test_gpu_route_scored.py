@@ -273,3 +273,68 @@ def test_offsets_past_32_bits():
     assert torch.equal(ids[-64:], i2) and torch.equal(w[-64:], w2)
     assert torch.equal(d[-64:], d2)
     assert (ids[:1000] == torch.arange(k, device="cuda")).all()
+
+
+def vanishing_logits(E, chosen):
+    """(logits, bias) of a softmax router whose bias lifts `chosen` experts
+    far below the row's largest logit: by 500 (scores that 64 bits hold), 800
+    and the type's lowest value (scores of 0), by an unchosen +inf, and with
+    one chosen expert at the top."""
+    import torch
+    l = torch.randn(8, E, generator=torch.Generator().manual_seed(17))
+    for row, drop in ((1, -500.0), (2, -800.0),
+                      (3, torch.finfo(torch.float32).min), (4, 0.0)):
+        l[row, chosen] += drop
+    l[4, (chosen[0] + 1) % E] = float("inf")
+    l[5, chosen] -= 900.0
+    l[5, chosen[1]] = 4.0
+    l[6] = torch.finfo(torch.float32).min      # equal shares
+    l[7, chosen] = float("-inf")
+    l[7, chosen[0]] = -2000.0
+    bias = torch.zeros(E)
+    bias[chosen] = 4.0
+    return l, bias
+
+
+@pytest.mark.parametrize("E,chosen", [(40, [39, 3, 17]), (12, [2, 3, 4]),
+                                      (256, [7, 200, 64, 65]),
+                                      (1000, [999, 0, 512])])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_of_vanishing_softmax_scores(E, chosen, dtype):
+    """Renormalised weights are the softmax over the k chosen, w: their
+    gradient is scale w_j (dw_j - sum_i dw_i w_i), and 0 in rows whose chosen
+    scores are all 0 in the softmax over the row, where the weights are 0."""
+    import torch
+    import expert_moe_fp32_amd as m
+    l, bias = vanishing_logits(E, chosen)
+    logits = (l if dtype == "f32" else l.clamp(
+        min=torch.finfo(torch.bfloat16).min).to(torch.bfloat16)).cuda()
+    T, k = l.shape[0], len(chosen)
+    r, ids, w, _ = route(logits, bias.cuda(), k, score="softmax", scale=2.5)
+    d_w = torch.randn(T, k, device="cuda",
+                      generator=torch.Generator("cuda").manual_seed(4))
+    d = torch.full((T, E), 9.0, device="cuda", dtype=logits.dtype)
+    m.moe_route_scored_backward(r, logits, ids, d_w, d)
+    torch.cuda.synchronize()
+    id64, dw = ids.cpu().numpy(), to_f64(d_w)
+    lj = np.take_along_axis(to_f64(logits), id64.astype(np.int64), 1)
+    rid, rw, _ = ob.route_scored(to_f64(logits), to_f64(bias), k,
+                                 score="softmax")
+    assert np.array_equal(id64, rid)
+    dead = (rw == 0).all(1)
+    assert dead[[2, 3]].all() and (to_f64(w)[dead] == 0).all()
+    top = lj.max(1, keepdims=True)
+    with np.errstate(invalid="ignore"):          # inf - inf
+        p = np.where(lj == top, 1.0, np.exp(lj - top))
+    p[lj == -np.inf] = 0.0
+    p[dead] = 0.0
+    p /= np.where(dead, 1.0, p.sum(1))[:, None]
+    part = 2.5 * p * (dw - (dw * p).sum(1, keepdims=True))
+    ref = np.zeros((T, E))
+    np.put_along_axis(ref, id64.astype(np.int64), part, 1)
+    big = 2.5 * np.abs(dw).sum(1, keepdims=True)
+    half = 2.0 ** -24 + (2.0 ** -8 if dtype == "bf16" else 0.0)
+    tol = np.abs(ref) * half * (1 + 1e-6) + 32 * 2.0 ** -53 * big * (ref != 0) \
+        + 2.0 ** -133
+    err = np.abs(to_f64(d) - ref)
+    assert (err <= tol).all(), np.argwhere(~(err <= tol))[:4].tolist()
