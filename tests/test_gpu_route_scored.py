@@ -338,3 +338,36 @@ def test_gradient_of_vanishing_softmax_scores(E, chosen, dtype):
         + 2.0 ** -133
     err = np.abs(to_f64(d) - ref)
     assert (err <= tol).all(), np.argwhere(~(err <= tol))[:4].tolist()
+
+
+@pytest.mark.parametrize("E", [16, 256])
+@pytest.mark.parametrize("at,dw_scale", [(-715.0, 1.0), (-680.0, 1e20),
+                                         (-300.0, 1e30)])
+def test_gradient_of_tiny_sigmoid_scores(E, at, dw_scale):
+    """Chosen scores near the end of 64 bits: 1 / S and dw / S pass its range,
+    the gradient w_j (dw_j - sum_i dw_i w_i) (1 - s_j) does not."""
+    import torch
+    import expert_moe_fp32_amd as m
+    k = 4
+    l = torch.full((6, E), float("-inf"))
+    g = torch.Generator().manual_seed(19)
+    l[:, ::2] = at + torch.rand(6, E // 2, generator=g)
+    logits = l.cuda()
+    r, ids, w, _ = route(logits, None, k, score="sigmoid", scale=1.5)
+    d_w = dw_scale * torch.randn(6, k, device="cuda", generator=torch.Generator(
+        "cuda").manual_seed(5))
+    d = torch.empty(6, E, device="cuda")
+    m.moe_route_scored_backward(r, logits, ids, d_w, d)
+    torch.cuda.synchronize()
+    id64, dw = ids.cpu().numpy().astype(np.int64), to_f64(d_w)
+    # sigmoid(l) = exp(l) and 1 - sigmoid(l) = 1 to 64 bits this far down
+    p = np.exp(np.take_along_axis(l.double().numpy(), id64, 1) - at)
+    p /= p.sum(1, keepdims=True)
+    part = 1.5 * p * (dw - (dw * p).sum(1, keepdims=True))
+    ref = np.zeros((6, E))
+    np.put_along_axis(ref, id64, part, 1)
+    # scores of exp(-715) are held in steps of 2^-1074: 2^-42 of them, which
+    # the weights, their sum and the products count a few times
+    big = 1.5 * np.abs(dw).sum(1, keepdims=True)
+    tol = np.abs(ref) * 2.0 ** -24 * (1 + 1e-6) + big * 2.0 ** -38 * (ref != 0)
+    assert (np.abs(to_f64(d) - ref) <= tol).all()
