@@ -604,7 +604,7 @@ moe_status moe_route_scored_workspace_size(const moe_router* r, size_t* bytes) {
   const moe_status st = moe_check_router(r);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
-  *bytes = route_scored_partials(r) * sizeof(int32_t);
+  *bytes = route_scored_scratch(r) * sizeof(int32_t);
   return MOE_OK;
 }
 
@@ -693,7 +693,7 @@ moe_status moe_residual_norm_workspace_size(const moe_norm* n, size_t* bytes) {
   const moe_status st = moe_check_norm(n);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
-  *bytes = norm_grad_partials(n) * sizeof(float);
+  *bytes = norm_grad_scratch(n) * sizeof(float);
   return MOE_OK;
 }
 

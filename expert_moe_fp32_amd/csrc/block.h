@@ -10,8 +10,10 @@ hipError_t launch_count_ids(const int32_t* ids, int n, int E, int32_t* counts,
                             hipStream_t s);
 
 // Scored routing.  `counts` (optional) needs route_scored_partials(...) int32
-// of scratch when that is not 0.
+// of scratch when that is not 0; route_scored_scratch(...) serves every batch
+// of up to T tokens.
 size_t route_scored_partials(const moe_router* r);
+size_t route_scored_scratch(const moe_router* r);
 hipError_t launch_route_scored(const moe_router* r, const void* logits,
                                const float* bias, int32_t* ids, float* w,
                                int32_t* counts, int32_t* partials,
@@ -57,6 +59,7 @@ struct NormGradArgs {
   float* d_pre;            // or null
 };
 size_t norm_grad_partials(const moe_norm* n);   // floats of scratch
+size_t norm_grad_scratch(const moe_norm* n);    // ... for up to T rows
 hipError_t launch_residual_norm_backward(const moe_norm* n,
                                          const NormGradArgs& a,
                                          float* partials, hipStream_t s);

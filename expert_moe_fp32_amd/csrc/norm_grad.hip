@@ -33,6 +33,7 @@ struct NormGradRun {
 };
 
 constexpr int kShare = 256;            // threads that short rows share
+constexpr int kAlone = 256;            // batches whose rows share none
 
 // FIT kExact: besides, every operand but the gate is there, so the row's code
 // has no branches (with a branch a piece and operand the 4096 x 7168 case ran
@@ -342,7 +343,7 @@ Shape grad_shape(int T, int H) {
   s.ept = v <= 512 ? 8 : 16;
   s.keep = v <= 1024;
   s.nt = ((H + s.ept - 1) / s.ept + 63) / 64 * 64;
-  s.rows = s.nt <= kShare / 2 && T > 256 ? kShare / s.nt : 1;
+  s.rows = s.nt <= kShare / 2 && T > kAlone ? kShare / s.nt : 1;
   const int per_cu = std::max(1, (s.ept == 8 ? 3 : 2) / ((s.nt * s.rows + 255) / 256));
   s.grid = (int)std::min<long>(((long)T + s.rows - 1) / s.rows, 256 * per_cu);
   return s;
@@ -369,6 +370,14 @@ void launch(const NormGradRun& q, const Shape& sh, hipStream_t s) {
 
 size_t norm_grad_partials(const moe_norm* n) {
   return (size_t)grad_shape(n->T, n->H).grid * (3 * (size_t)n->H + 1);
+}
+
+// Workgroups grow with T but for one step down, where short rows begin to
+// share them.
+size_t norm_grad_scratch(const moe_norm* n) {
+  moe_norm few = *n;
+  few.T = std::min(n->T, kAlone);
+  return std::max(norm_grad_partials(n), norm_grad_partials(&few));
 }
 
 hipError_t launch_residual_norm_backward(const moe_norm* n,

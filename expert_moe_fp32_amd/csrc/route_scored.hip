@@ -732,6 +732,7 @@ RouteArgs route_args(const moe_router* r, const void* logits) {
 // spread over the CUs; the wavefronts that stay on the GPU at once walk larger
 // batches (128 tokens of 256 experts with counts: 7.1 us, 8.1 with 8
 // wavefronts a workgroup throughout).
+constexpr int kCus = 256;
 struct RouteShape {
   int waves, grid;
 };
@@ -739,8 +740,8 @@ RouteShape route_shape(const moe_router* r) {
   const int segs = 64 / lanes_of(r);
   const long w = ((long)r->T + segs - 1) / segs;
   RouteShape s;
-  s.waves = (int)(w <= kWaves ? w : std::min<long>((w + 255) / 256, kWaves));
-  s.grid = (int)std::min<long>((w + s.waves - 1) / s.waves, 512);
+  s.waves = (int)(w <= kWaves ? w : std::min<long>((w + kCus - 1) / kCus, kWaves));
+  s.grid = (int)std::min<long>((w + s.waves - 1) / s.waves, 2 * kCus);
   return s;
 }
 
@@ -757,6 +758,13 @@ size_t route_scored_partials(const moe_router* r) {
   if (r->T == 0) return 0;
   const RouteShape s = route_shape(r);
   return sums_counts(r, s) ? (size_t)s.grid * r->E : 0;
+}
+
+// The grid falls whenever the wavefronts a workgroup grow: below kCus
+// workgroups until they are kWaves, then it grows with T to its end.
+size_t route_scored_scratch(const moe_router* r) {
+  if (!route_scored_partials(r)) return 0;
+  return (size_t)std::max(kCus, route_shape(r).grid) * r->E;
 }
 
 hipError_t launch_route_scored(const moe_router* r, const void* logits,

@@ -290,8 +290,9 @@ typedef struct {
 /* Validate a router description (host only). */
 MOE_API moe_status moe_check_router(const moe_router* r);
 
-/* Bytes of scratch moe_route_scored needs when it counts the experts (host
- * only; 256-byte aligned device memory; 0 for small batches). */
+/* Bytes of scratch moe_route_scored needs when it counts the experts of this
+ * batch or of a smaller T (host only; 256-byte aligned device memory; 0 for
+ * small batches). */
 MOE_API moe_status moe_route_scored_workspace_size(const moe_router* r,
                                                    size_t* bytes);
 
@@ -393,8 +394,8 @@ MOE_API moe_status moe_residual_norm(const moe_norm* n, const void* y,
                                      void* resid_out, void* x_out,
                                      void* stream);
 
-/* Bytes of scratch of moe_residual_norm_backward (host only; 256-byte aligned
- * device memory, not initialised). */
+/* Bytes of scratch of moe_residual_norm_backward for this batch or a smaller
+ * T (host only; 256-byte aligned device memory, not initialised). */
 MOE_API moe_status moe_residual_norm_workspace_size(const moe_norm* n,
                                                     size_t* bytes);
 

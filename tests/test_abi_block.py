@@ -355,3 +355,19 @@ def test_layer_buffers_take_no_other_routing(monkeypatch, size):
     for fits in ((8, 16, 4), (4, 16, 4), (8, 8, 4)):
         assert dl.route_scored(Anything(), m.make_router(*fits), P,
                                None) == "called"
+
+
+def test_a_buffer_for_many_rows_serves_fewer():
+    """Workspaces never shrink as T grows, and a call takes the buffer that
+    the query gave for a larger batch."""
+    edges = sorted({0, 1, 2, 8, 9, 64, 4097, 8192, 9001, 20000, 100000} | {
+        t + d for t in (128, 256, 320, 512, 768, 1024, 1280, 1792, 2048, 4096)
+        for d in (-1, 0, 1, 2, 3, 40)})
+    for H in (1, 64, 72, 512, 520, 1000, 1024, 1032, 2501, 4096, 4104, 7168,
+              8192, 8200, 16384):
+        size = [m.moe_residual_norm_workspace_size(norm(T=t, H=H)) for t in edges]
+        assert size == sorted(size), H
+    for E, k in ((8, 2), (64, 6), (65, 8), (256, 16), (256, 8), (1000, 1)):
+        size = [m.moe_route_scored_workspace_size(m.make_router(t, E, k))
+                for t in edges]
+        assert size == sorted(size), (E, k)

@@ -219,3 +219,24 @@ def test_offsets_past_32_bits():
                                  d_y2, d_r2, None, None, None, ws, ws.numel())
     torch.cuda.synchronize()
     assert torch.equal(d_y[-16:], d_y2) and torch.equal(d_r[-16:], d_r2)
+
+
+def test_one_workspace_for_every_batch():
+    """A buffer of the largest batch's size serves the smaller ones."""
+    import torch
+    import expert_moe_fp32_amd as m
+    size = m.moe_residual_norm_workspace_size(m.make_norm(1000, 512))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for T in (1000, 257, 256, 3):
+        c = NormCase(T, 512, seed=10)
+        c.forward()
+        d_x, outs = c.rows("bf16", 0), []
+        for w in (ws, torch.empty(m.moe_residual_norm_workspace_size(c.n),
+                                  dtype=torch.uint8, device="cuda")):
+            d_r, d_pre = c.rows("bf16", 0), torch.empty(512, device="cuda")
+            m.moe_residual_norm_backward(c.n, c.y, c.resid_out, c.post, None,
+                                         c.pre, d_x, None, None, d_r, None,
+                                         None, d_pre, w, w.numel())
+            outs.append((d_r[:T], d_pre))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
