@@ -446,15 +446,23 @@ def make_norm(T, H, block="bf16", resid="bf16", out="bf16", gain="f32",
                 eps, gain_offset, residual_scale, rows, cols, *strides)
 
 
-def _enqueue(name, first, stream, check, *args) -> int:
+def _enqueue(name, arrays, stream, check, *args) -> int:
     """Call an entry point on ``stream``, or on the current stream of the
-    device that holds ``first`` (with that device current)."""
+    device that holds ``arrays`` (with that device current): the first of
+    them that is a device tensor tells (a batch of no rows may come without
+    most of them)."""
     fn = getattr(_lib or lib(), name)
+    on = None
+    if stream is None:
+        for a in arrays:
+            if getattr(a, "is_cuda", False):
+                on = a
+                break
     if stream is not None:
         st = fn(*args, stream)
-    elif getattr(first, "is_cuda", False):
+    elif on is not None:
         import torch
-        dev = first.device.index
+        dev = on.device.index
         if dev == torch.cuda.current_device():
             st = fn(*args, _raw_stream(dev))
         else:
@@ -497,21 +505,25 @@ def moe_residual_norm_workspace_size(n: Norm) -> int:
 def moe_route_scored(r: Router, logits, bias, topk_ids, topk_w,
                      expert_counts=None, workspace=None, ws_bytes=0,
                      stream=None, check=True) -> int:
-    return _enqueue("moe_route_scored", logits, stream, check,
+    return _enqueue("moe_route_scored", (logits, bias, topk_ids, topk_w,
+                                         expert_counts, workspace),
+                    stream, check,
                     ctypes.byref(r), ptr(logits), ptr(bias), ptr(topk_ids),
                     ptr(topk_w), ptr(expert_counts), ptr(workspace), ws_bytes)
 
 
 def moe_route_scored_backward(r: Router, logits, topk_ids, d_topk_w, d_logits,
                               stream=None, check=True) -> int:
-    return _enqueue("moe_route_scored_backward", logits, stream, check,
+    return _enqueue("moe_route_scored_backward",
+                    (logits, topk_ids, d_topk_w, d_logits), stream, check,
                     ctypes.byref(r), ptr(logits), ptr(topk_ids),
                     ptr(d_topk_w), ptr(d_logits))
 
 
 def moe_residual_norm(n: Norm, y, resid, post_gain, gate, pre_gain, resid_out,
                       x_out, stream=None, check=True) -> int:
-    return _enqueue("moe_residual_norm", resid, stream, check,
+    return _enqueue("moe_residual_norm", (resid, y, post_gain, gate, pre_gain,
+                                          resid_out, x_out), stream, check,
                     ctypes.byref(n), ptr(y), ptr(resid), ptr(post_gain),
                     ptr(gate), ptr(pre_gain), ptr(resid_out), ptr(x_out))
 
@@ -520,7 +532,10 @@ def moe_residual_norm_backward(n: Norm, y, resid_out, post_gain, gate,
                                pre_gain, d_x, d_resid_out, d_y, d_resid,
                                d_post_gain, d_gate, d_pre_gain, workspace,
                                ws_bytes, stream=None, check=True) -> int:
-    return _enqueue("moe_residual_norm_backward", workspace, stream, check,
+    return _enqueue("moe_residual_norm_backward",
+                    (workspace, y, resid_out, post_gain, gate, pre_gain, d_x,
+                     d_resid_out, d_y, d_resid, d_post_gain, d_gate,
+                     d_pre_gain), stream, check,
                     ctypes.byref(n), ptr(y), ptr(resid_out), ptr(post_gain),
                     ptr(gate), ptr(pre_gain), ptr(d_x), ptr(d_resid_out),
                     ptr(d_y), ptr(d_resid), ptr(d_post_gain), ptr(d_gate),
@@ -530,7 +545,10 @@ def moe_residual_norm_backward(n: Norm, y, resid_out, post_gain, gate,
 def moe_combine_norm(p: Problem, n: Norm, y_perm, pair_row, topk_w, y_shared,
                      resid, post_gain, gate, pre_gain, block_out, resid_out,
                      x_out, stream=None, check=True) -> int:
-    return _enqueue("moe_combine_norm", y_perm, stream, check,
+    return _enqueue("moe_combine_norm",
+                    (y_perm, pair_row, topk_w, y_shared, resid, post_gain,
+                     gate, pre_gain, block_out, resid_out, x_out),
+                    stream, check,
                     ctypes.byref(p), ctypes.byref(n), ptr(y_perm),
                     ptr(pair_row), ptr(topk_w), ptr(y_shared), ptr(resid),
                     ptr(post_gain), ptr(gate), ptr(pre_gain), ptr(block_out),
@@ -540,7 +558,9 @@ def moe_combine_norm(p: Problem, n: Norm, y_perm, pair_row, topk_w, y_shared,
 def moe_combine_backward(p: Problem, d_out, y_perm, pair_row, topk_w,
                          d_y_perm, d_topk_w, d_y_shared, stream=None,
                          check=True) -> int:
-    return _enqueue("moe_combine_backward", d_out, stream, check,
+    return _enqueue("moe_combine_backward",
+                    (d_out, y_perm, pair_row, topk_w, d_y_perm, d_topk_w,
+                     d_y_shared), stream, check,
                     ctypes.byref(p), ptr(d_out), ptr(y_perm), ptr(pair_row),
                     ptr(topk_w), ptr(d_y_perm), ptr(d_topk_w),
                     ptr(d_y_shared))
@@ -551,7 +571,10 @@ def moe_layer_forward_scored(p: Problem, r: Router, n: Optional[Norm], logits,
                              resid, post_gain, gate, pre_gain, out, resid_out,
                              x_out, expert_counts, workspace, ws_bytes,
                              stream=None, check=True) -> int:
-    return _enqueue("moe_layer_forward_scored", x, stream, check,
+    return _enqueue("moe_layer_forward_scored",
+                    (x, logits, bias, l2p, replica_count, resid, post_gain,
+                     gate, pre_gain, out, resid_out, x_out, expert_counts,
+                     workspace), stream, check,
                     ctypes.byref(p), ctypes.byref(r),
                     None if n is None else ctypes.byref(n), ptr(logits),
                     ptr(bias), ptr(x), ctypes.byref(weights), ptr(l2p),

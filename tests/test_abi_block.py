@@ -371,3 +371,61 @@ def test_a_buffer_for_many_rows_serves_fewer():
         size = [m.moe_route_scored_workspace_size(m.make_router(t, E, k))
                 for t in edges]
         assert size == sorted(size), (E, k)
+
+
+def test_any_array_names_the_device(monkeypatch):
+    """A batch of no rows may come without the arrays that usually name the
+    device; the sums that it clears name it as well."""
+    import contextlib
+
+    import torch
+
+    class OnDevice1:
+        is_cuda = True
+        device = torch.device("cuda", 1)
+
+        def data_ptr(self):
+            return P
+
+    seen = []
+
+    @contextlib.contextmanager
+    def device(d):
+        seen.append(d)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(L, "_raw_stream", lambda d: d)
+    calls = {}
+
+    class Library:                         # nothing is launched
+        def __getattr__(self, name):
+            def call(*args):
+                calls[name] = args[-1]
+                return L.MOE_OK
+            call.__name__ = name
+            return call
+
+    monkeypatch.setattr(L, "_lib", Library())
+    monkeypatch.setattr(L, "lib", lambda: L._lib)
+    n, r, p, w = norm(T=0), router(T=0), problem(T=0), L.Weights()
+    # (name, call on a list of arrays, how many)
+    for name, count, call in (
+            ("moe_route_scored", 6, lambda a: m.moe_route_scored(r, *a)),
+            ("moe_route_scored_backward", 4,
+             lambda a: m.moe_route_scored_backward(r, *a)),
+            ("moe_residual_norm", 7, lambda a: m.moe_residual_norm(n, *a)),
+            ("moe_residual_norm_backward", 13,
+             lambda a: m.moe_residual_norm_backward(n, *a, 0)),
+            ("moe_combine_norm", 11, lambda a: m.moe_combine_norm(p, n, *a)),
+            ("moe_combine_backward", 7,
+             lambda a: m.moe_combine_backward(p, *a)),
+            ("moe_layer_forward_scored", 14, lambda a:
+             m.moe_layer_forward_scored(p, r, n, *a[:3], w, *a[3:], 0))):
+        for at in range(count):
+            arrays = [None] * count
+            arrays[at] = OnDevice1()
+            del seen[:]
+            call(arrays)
+            assert seen == [1] and calls[name] == 1, (name, at)
