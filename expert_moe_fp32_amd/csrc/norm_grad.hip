@@ -86,7 +86,8 @@ __global__ __launch_bounds__(KEEP ? 512 : 1024) void k_residual_norm_backward(No
   Raw<RT, W> gq[P], rq[P];
   Raw<YT, W> yq[P];
   u32x4_t xq[P];
-  // (a row past the end reads the last one again, adds zero and stores nothing)
+  // (a row past the end reads the last one again and takes part in the
+  // exchanges alone: zero times an infinity would not add zero)
   const long last = n.T - 1;
   auto fetch = [&](long t) {
     t = min(t, last);
@@ -151,8 +152,7 @@ __global__ __launch_bounds__(KEEP ? 512 : 1024) void k_residual_norm_backward(No
   // every row of a workgroup takes part in its barriers, past the end too
   for (long t0 = (long)blockIdx.x * R; t0 < n.T; t0 += step, par ^= 1) {
     const long t = t0 + rg;
-    const bool valid = t < n.T;
-    const float live = valid ? 1.0f : 0.0f;
+    const bool valid = EPT == 16 || t < n.T;   // (only short rows share)
     if (!KEEP) fetch(t);
     V g[P];
     Raw<RT, W> r[P];
@@ -177,43 +177,43 @@ __global__ __launch_bounds__(KEEP ? 512 : 1024) void k_residual_norm_backward(No
     const float ys = has_post ? 1.0f / sqrtf(s[2] * inv_h + n.eps) : 1.0f;
     const float ysr = ys * n.residual_scale;
     float s2[2] = {0.0f, 0.0f};        // q y ys, the gate's row
-    const float gate1 = !GV && a.gate ? a.gate[n.gate_rows > 1 ? min(t, last) : 0] : 1.0f;
-    // a row past the end adds nothing to the sums
-    const float rsl = rs * live, ysl = ysr * live;
+    if (valid) {
+      const float gate1 = !GV && a.gate ? a.gate[n.gate_rows > 1 ? t : 0] : 1.0f;
 #pragma unroll
-    for (int v = 0; v < P; ++v) {
-      const V rv = widen<RT, W>(r[v]), xv = wide_x(x[v], v);
-      const V yv = widen<YT, W>(y[v]) * ysl;     // unit(y) rscale
-      const V po = post_of(v);
-      if constexpr (KEEP) d_pre[v] += xv * (rv * rsl);
-      else lds_pre[tid + v * NT] += xv * (rv * rsl);
-      g[v] += rs * (xv * pre_of(v) - c * rv);
-      if (valid && (FULL || a.d_resid))
-        store_piece<RT, W, FIT, true>((RT*)a.d_resid + t * n.resid_stride, pc[v], H, g[v]);
-      if (!to_block) continue;
-      V h = g[v] * yv;                 // what the gate's gradient sums, less po
-      if constexpr (GV) {
-        const V f = load_f32<W, FIT>(a.gate + (n.gate_rows > 1 ? min(t, last) * H : 0), pc[v], H);
-        if (q.col_gate) {
-          d_gc[v] += h * po;
-        } else if (a.d_gate && valid) {
-          const V e = h * po;
+      for (int v = 0; v < P; ++v) {
+        const V rv = widen<RT, W>(r[v]), xv = wide_x(x[v], v);
+        const V yv = widen<YT, W>(y[v]) * ysr;     // unit(y) rscale
+        const V po = post_of(v);
+        if constexpr (KEEP) d_pre[v] += xv * (rv * rs);
+        else lds_pre[tid + v * NT] += xv * (rv * rs);
+        g[v] += rs * (xv * pre_of(v) - c * rv);
+        if (FULL || a.d_resid)
+          store_piece<RT, W, FIT, true>((RT*)a.d_resid + t * n.resid_stride, pc[v], H, g[v]);
+        if (!to_block) continue;
+        V h = g[v] * yv;                 // what the gate's gradient sums, less po
+        if constexpr (GV) {
+          const V f = load_f32<W, FIT>(a.gate + (n.gate_rows > 1 ? t * H : 0), pc[v], H);
+          if (q.col_gate) {
+            d_gc[v] += h * po;
+          } else if (a.d_gate) {
+            const V e = h * po;
 #pragma unroll
-          for (int i = 0; i < W; i += 4)
-            store_piece<float, 4, FIT, true>(a.d_gate + t * H, piece_at<4, FIT>(pc[v].col + i, H), H,
-                                             f32x4_t{e[i], e[i + 1], e[i + 2], e[i + 3]});
+            for (int i = 0; i < W; i += 4)
+              store_piece<float, 4, FIT, true>(a.d_gate + t * H, piece_at<4, FIT>(pc[v].col + i, H), H,
+                                               f32x4_t{e[i], e[i + 1], e[i + 2], e[i + 3]});
+          }
+          h *= f;
+          g[v] *= f;
+        } else {
+          s2[1] += dot_cols<W>(h, po);
+          h *= gate1;
+          g[v] *= gate1;
         }
-        h *= f;
-        g[v] *= f;
-      } else {
-        s2[1] += dot_cols<W>(h, po);
-        h *= gate1;
-        g[v] *= gate1;
+        if constexpr (KEEP) d_post[v] += h;
+        else lds_post[tid + v * NT] += h;
+        s2[0] += dot_cols<W>(h, po);
+        g[v] *= po;
       }
-      if constexpr (KEEP) d_post[v] += h;
-      else lds_post[tid + v * NT] += h;
-      s2[0] += dot_cols<W>(h, po);
-      g[v] *= po;
     }
     if (!to_block) continue;
     if (has_post || row_gate) row_sum(s2, red2[par], first, waves);

@@ -240,3 +240,37 @@ def test_one_workspace_for_every_batch():
             outs.append((d_r[:T], d_pre))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("T,H,post,gate", [
+    (1031, 512, True, "scalar"), (258, 256, False, None),
+    (261, 72, True, "channel")])
+def test_infinite_gradient_in_the_last_row(T, H, post, gate):
+    """An infinity in the last row's d_x reaches its own column's d_pre as an
+    infinity, whatever the number of rows that share a workgroup; the other
+    columns stay as they are."""
+    import torch
+    import expert_moe_fp32_amd as m
+    c = NormCase(T, H, post=post, gate=gate, seed=9)
+    c.forward()
+    d_x = c.rows("bf16", 0)
+    size = m.moe_residual_norm_workspace_size(c.n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def d_pre():
+        out = torch.empty(H, device="cuda")
+        m.moe_residual_norm_backward(
+            c.n, c.y, c.resid_out, c.post, c.gate, c.pre, d_x, None,
+            c.rows("bf16", 0), c.rows("bf16", 0), None, None, out, ws, size)
+        torch.cuda.synchronize()
+        return out
+
+    at = H // 2 + 1
+    assert c.resid_out[T - 1, at] != 0
+    ref = d_pre()
+    d_x[T - 1, at] = float("inf")
+    got = d_pre()
+    sign = float(torch.sign(c.resid_out[T - 1, at].float()))
+    assert float(got[at]) == sign * float("inf")
+    keep = torch.arange(H, device="cuda") != at
+    assert torch.equal(got[keep], ref[keep])
