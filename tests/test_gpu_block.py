@@ -374,3 +374,89 @@ def test_two_streams_at_once():
     for (b, _), r in zip(pairs, ref):
         for n, v in b.outputs().items():
             assert torch.equal(v, r[n]), n
+
+
+def layer_arrays(wl, gate, seed=71):
+    """(router, bias, logits, x, norm case, its outputs) of a scored layer
+    that ends in a norm with a gate."""
+    import torch
+    import expert_moe_fp32_amd as m
+    from expert_moe_fp32_amd.runner import to_dev
+    router = m.make_router(wl.T, wl.E, wl.k, "sigmoid", 4, 2, 2, scale=2.5)
+    bias = (0.1 * torch.randn(wl.E, generator=torch.Generator()
+                              .manual_seed(seed))).cuda()
+    c = NormCase(wl.T, wl.H, block=wl.out, gate=gate, rscale=0.5, seed=seed)
+    outs = [torch.full((wl.T, wl.H), 3.0, dtype=torch.bfloat16, device="cuda")
+            for _ in range(2)]
+    return router, bias, to_dev(wl.logits), to_dev(wl.x), c, outs
+
+
+@pytest.mark.parametrize("gate", ["token", "channel"])
+def test_scored_layer_with_replicas_and_a_gate(gate):
+    """As test_scored_layer_equals_its_steps, some experts held twice."""
+    import torch
+    from oracle import eplb
+    from .helpers import phys_to_logical_from_map
+    wl = make_workload("prefill", seed=33, T=200, H=256, I=256, E=16,
+                       num_local=8, k=4)
+    l2p, rep, P = eplb.hottest_replica_map(np.arange(8) ** 2, 3)
+    dl = device_layer(wl, l2p=l2p, rep=rep, P=P,
+                      phys_to_logical=phys_to_logical_from_map(l2p, rep, P))
+    router, bias, logits, x, c, (ro, xo) = layer_arrays(wl, gate)
+    b, s = dl.buffers(), dl.buffers()
+    dl.forward_scored(b, router, logits, bias, x, c.n, c.resid, c.post, c.gate,
+                      c.pre, ro, xo)
+    dl.route_scored(s, router, logits, bias)
+    dl.dispatch(s, x)
+    dl.ffn(s, x_shared=x if wl.shared else None)
+    ro2, xo2 = torch.empty_like(ro), torch.empty_like(xo)
+    dl.combine_norm(s, c.n, c.resid, c.post, c.gate, c.pre, ro2, xo2)
+    torch.cuda.synchronize()
+    assert torch.equal(s.counts, b.counts) and torch.equal(s.out, b.out)
+    assert torch.equal(ro, ro2) and torch.equal(xo, xo2)
+
+
+@pytest.mark.parametrize("name,kw,shared", LAYERS[:3])
+def test_scored_layer_replays_from_a_graph(name, kw, shared):
+    """The layer captured; replays with eager work between them equal the
+    eager call bit for bit, also after its inputs change."""
+    import torch
+    wl = make_workload(name, seed=34, **kw)
+    dl = device_layer(wl)
+    router, bias, logits, x, c, (ro, xo) = layer_arrays(wl, "token")
+    b, other = dl.buffers(), dl.buffers()
+
+    def call(buffers=b, l=logits, out=(ro, xo)):
+        dl.forward_scored(buffers, router, l, bias, x, c.n, c.resid, c.post,
+                          c.gate, c.pre, *out)
+
+    def outputs():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (ro, xo, b.out, b.counts)]
+
+    call()
+    eager = outputs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    flipped = logits.flip(0).contiguous()
+    aside = [torch.empty_like(ro), torch.empty_like(xo)]
+    for r in range(4):
+        for t in (ro, xo, b.out, b.counts):
+            t.zero_()
+        graph.replay()
+        for i, (got, ref) in enumerate(zip(outputs(), eager)):
+            assert torch.equal(got, ref), (r, i)
+        call(other, flipped, aside)
+        torch.cuda.synchronize()
+    logits.copy_(flipped)
+    call()
+    eager = outputs()
+    graph.replay()
+    assert all(torch.equal(g, e) for g, e in zip(outputs(), eager))

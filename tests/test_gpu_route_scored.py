@@ -371,3 +371,22 @@ def test_gradient_of_tiny_sigmoid_scores(E, at, dw_scale):
     big = 1.5 * np.abs(dw).sum(1, keepdims=True)
     tol = np.abs(ref) * 2.0 ** -24 * (1 + 1e-6) + big * 2.0 ** -38 * (ref != 0)
     assert (np.abs(to_f64(d) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("shape", [  # T, E, k, groups, topk_groups, group_top
+    (4100, 256, 8, 8, 4, 2), (8195, 256, 8, 8, 4, 2),
+    (4500, 1000, 4, 8, 3, 2),      # groups of 125: eight wavefronts' scratch
+    (4300, 100, 5, 4, 2, 2), (1500, 90, 6, 1, 1, 1),
+    (16500, 60, 4, 5, 2, 2),       # four tokens a wavefront
+], ids=str)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_more_tokens_than_wavefronts(shape, score):
+    """Batches whose wavefronts walk on to a second token and whose counts
+    are summed over the workgroups, of any number of experts."""
+    import torch
+    T, E, k, G, keep, top = shape
+    print(shape, score, flush=True)
+    logits = make_logits(T, E, "f32", 41, masked=0.02).cuda()
+    bias = (0.1 * torch.randn(E, generator=torch.Generator().manual_seed(6))).cuda()
+    check_route(logits, bias, k, score=score, groups=G, topk_groups=keep,
+                group_top=top, scale=2.5)
