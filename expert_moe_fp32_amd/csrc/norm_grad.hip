@@ -152,7 +152,7 @@ __global__ __launch_bounds__(KEEP ? 512 : 1024) void k_residual_norm_backward(No
   // every row of a workgroup takes part in its barriers, past the end too
   for (long t0 = (long)blockIdx.x * R; t0 < n.T; t0 += step, par ^= 1) {
     const long t = t0 + rg;
-    const bool valid = EPT == 16 || t < n.T;   // (only short rows share)
+    const bool valid = !KEEP || t < n.T;       // (long rows share no workgroup)
     if (!KEEP) fetch(t);
     V g[P];
     Raw<RT, W> r[P];
