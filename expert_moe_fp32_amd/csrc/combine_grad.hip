@@ -3,8 +3,8 @@
 // A workgroup holds its token's d_out row in registers, walks the token's
 // local slots, and for each reads the expert row once for the weight's
 // gradient and writes the row's gradient.  Bound by HBM, per local row H * 4
-// bytes in and out: 4096 x 7168, 32 of 256 experts here and a shared one, 79
-// us = 5.2 TB/s (one piece of four columns at a time and sums through LDS: 98
+// bytes in and out: 4096 x 7168, 32 of 256 experts here and a shared one, 80
+// us = 5.1 TB/s (one piece of four columns at a time and sums through LDS: 98
 // us).
 #include <type_traits>
 

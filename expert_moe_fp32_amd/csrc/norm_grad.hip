@@ -11,7 +11,7 @@
 // and of a gate along the columns add up in registers over a workgroup's
 // rows; a second launch sums the workgroups' rows in a fixed order.  Bound by
 // HBM, four rows in and two out, and by the one workgroup of a long row that a
-// CU's registers hold: 4096 x 7168 bf16 with all operands 72 us = 4.9 TB/s,
+// CU's registers hold: 4096 x 7168 bf16 with all operands 76 us = 4.7 TB/s,
 // and 5 us for the column sums (16 slices a column; 4 took 40 us).
 #include <algorithm>
 #include <type_traits>
@@ -40,8 +40,10 @@ constexpr int kAlone = 256;            // batches whose rows share none
 // 103 us instead of 79: 1100 instructions a wavefront and row).
 // KEEP: the next row is requested early.  Rows too long for that (H > 8192)
 // take 1024 threads, which have half the registers: they do without, hold the
-// gains' sums in LDS and read the gains anew.
-// GV: a gate along the columns.
+// gains' sums in LDS, read the gains anew and spill 47 to 164 registers
+// (2048 x 16384 bf16 164 us = 2.5 TB/s).
+// GV: a gate along the columns; with 16 columns in pieces of four it spills 5
+// to 39 registers (4096 x 7168 float32 171 us, 131 us without a gate).
 template <typename YT, typename RT, int W, int EPT, Fit FIT, bool KEEP,
           bool GV>
 __global__ __launch_bounds__(KEEP ? 512 : 1024) void k_residual_norm_backward(NormGradRun q) {

@@ -332,8 +332,9 @@ MOE_API moe_status moe_route_scored(const moe_router* r, const void* logits,
  *   otherwise    ds_j = scale dw_j
  *   sigmoid: dl_e = ds_j s_j (1 - s_j) for the expert of slot j, else 0
  *   softmax: dl_e = s_e (ds_j [e in slot j] - sum_i ds_i s_i)
- * evaluated in 64 bits and rounded once.  Experts with a logit of -inf or NaN
- * get 0, and so do rows whose S is 0 under renormalize.
+ * evaluated in 64 bits and rounded to float32, and from that to bf16 for bf16
+ * logits.  Experts with a logit of -inf or NaN get 0, and so do rows whose S
+ * is 0 under renormalize.
  *   topk_ids [T][k] as moe_route_scored gave them (an id outside [0, E) gets
  *            no gradient)
  *   d_topk_w [T][k] float32
