@@ -41,7 +41,11 @@ EXPORTS = (
     "moe_route_scored_backward", "moe_check_norm", "moe_residual_norm",
     "moe_residual_norm_workspace_size", "moe_residual_norm_backward",
     "moe_combine_norm", "moe_combine_backward", "moe_layer_forward_scored",
+    "moe_layer_few_workspace_size", "moe_layer_forward_few", "moe_check_rows",
+    "moe_checkpoint_rows", "moe_restore_rows", "moe_experts_workspace_size",
+    "moe_experts_forward", "moe_experts_backward",
 )
+MOE_FEW_TOKENS = 16
 MOE_STAGE_EVENTS = 8
 STAGES = ("route", "dispatch_index", "gather", "tiles", "gate_up", "down",
           "combine")
@@ -81,6 +85,23 @@ class Norm(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("gate_rows", "gate_cols")] + [
         (n, ctypes.c_int64) for n in ("block_stride", "resid_stride",
                                       "resid_out_stride", "out_stride")]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "dtype")] + [
+        ("stride", ctypes.c_int64)]
+
+
+class Saved(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "offsets", "row_token", "row_weight", "pair_row", "x_codes",
+        "x_scales", "gu_codes", "gu_scales")]
+
+
+class WeightGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "d_gate", "d_up", "d_down", "sh_d_gate", "sh_d_up", "sh_d_down")] + [
+        ("dtype", ctypes.c_int32)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -157,6 +178,22 @@ def lib() -> ctypes.CDLL:
             "moe_layer_forward_scored": (ctypes.c_int, [
                 P, R, N, V, V, V, ctypes.POINTER(Weights)] + [V] * 11 +
                 [S, V]),
+            "moe_layer_few_workspace_size": (ctypes.c_int, [
+                P, ctypes.POINTER(S)]),
+            "moe_layer_forward_few": (ctypes.c_int, [
+                P, R, V, V, V, ctypes.POINTER(Weights)] + [V] * 5 + [S, V]),
+            "moe_check_rows": (ctypes.c_int, [ctypes.POINTER(Rows)]),
+            "moe_checkpoint_rows": (ctypes.c_int, [ctypes.POINTER(Rows)] +
+                                    [V] * 4),
+            "moe_restore_rows": (ctypes.c_int, [ctypes.POINTER(Rows)] +
+                                 [V] * 4),
+            "moe_experts_workspace_size": (ctypes.c_int, [
+                P, ctypes.POINTER(S)]),
+            "moe_experts_forward": (ctypes.c_int, [P] + [V] * 5 + [
+                ctypes.POINTER(Weights), ctypes.POINTER(Saved), V, V, S, V]),
+            "moe_experts_backward": (ctypes.c_int, [
+                P, ctypes.POINTER(Saved), V, ctypes.POINTER(Weights), V, V,
+                ctypes.POINTER(WeightGrads), V, S, V]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -581,6 +618,92 @@ def moe_layer_forward_scored(p: Problem, r: Router, n: Optional[Norm], logits,
                     ptr(replica_count), ptr(resid), ptr(post_gain), ptr(gate),
                     ptr(pre_gain), ptr(out), ptr(resid_out), ptr(x_out),
                     ptr(expert_counts), ptr(workspace), ws_bytes)
+
+
+# --------------- a few tokens, 8-bit checkpoints, training the experts
+def make_rows(rows, cols, dtype="bf16", stride=None) -> Rows:
+    return Rows(rows, cols, DTYPES[dtype], cols if stride is None else stride)
+
+
+def make_saved(offsets, row_token, row_weight, pair_row, x_codes, x_scales,
+               gu_codes, gu_scales) -> Saved:
+    """What the experts' forward pass leaves for the backward: tensors of the
+    shapes in include/moe.h, kept alive by the struct."""
+    tensors = (offsets, row_token, row_weight, pair_row, x_codes, x_scales,
+               gu_codes, gu_scales)
+    s = Saved(*[ptr(t) for t in tensors])
+    s.keep = tensors
+    return s
+
+
+def make_weight_grads(d_gate, d_up, d_down, dtype="f32", sh_gate=None,
+                      sh_up=None, sh_down=None) -> WeightGrads:
+    """Arrays of the experts' weight gradients, kept alive by the struct."""
+    tensors = (d_gate, d_up, d_down, sh_gate, sh_up, sh_down)
+    g = WeightGrads(*[ptr(t) for t in tensors], DTYPES[dtype])
+    g.keep = tensors
+    return g
+
+
+def moe_check_rows(r: Rows) -> int:
+    return lib().moe_check_rows(ctypes.byref(r))
+
+
+def moe_layer_few_workspace_size(p: Problem) -> int:
+    return _ws(lib().moe_layer_few_workspace_size, p)
+
+
+def moe_experts_workspace_size(p: Problem) -> int:
+    return _ws(lib().moe_experts_workspace_size, p)
+
+
+def moe_layer_forward_few(p: Problem, r: Optional[Router], logits, bias, x,
+                          weights: Weights, l2p, replica_count, out,
+                          expert_counts, workspace, ws_bytes, stream=None,
+                          check=True) -> int:
+    return _enqueue("moe_layer_forward_few",
+                    (x, logits, bias, l2p, replica_count, out, expert_counts,
+                     workspace), stream, check,
+                    ctypes.byref(p), None if r is None else ctypes.byref(r),
+                    ptr(logits), ptr(bias), ptr(x), ctypes.byref(weights),
+                    ptr(l2p), ptr(replica_count), ptr(out),
+                    ptr(expert_counts), ptr(workspace), ws_bytes)
+
+
+def moe_checkpoint_rows(r: Rows, src, codes, scales, stream=None,
+                        check=True) -> int:
+    return _enqueue("moe_checkpoint_rows", (src, codes, scales), stream,
+                    check, ctypes.byref(r), ptr(src), ptr(codes), ptr(scales))
+
+
+def moe_restore_rows(r: Rows, codes, scales, dst, stream=None,
+                     check=True) -> int:
+    return _enqueue("moe_restore_rows", (dst, codes, scales), stream, check,
+                    ctypes.byref(r), ptr(codes), ptr(scales), ptr(dst))
+
+
+def moe_experts_forward(p: Problem, x, topk_ids, topk_w, l2p, replica_count,
+                        weights: Weights, saved: Saved, out, workspace,
+                        ws_bytes, stream=None, check=True) -> int:
+    return _enqueue("moe_experts_forward",
+                    (x, topk_ids, topk_w, l2p, replica_count, out, workspace),
+                    stream, check,
+                    ctypes.byref(p), ptr(x), ptr(topk_ids), ptr(topk_w),
+                    ptr(l2p), ptr(replica_count), ctypes.byref(weights),
+                    ctypes.byref(saved), ptr(out), ptr(workspace), ws_bytes)
+
+
+def moe_experts_backward(p: Problem, saved: Saved, d_out, weights: Weights,
+                         d_x, d_topk_w, grads: Optional[WeightGrads],
+                         workspace, ws_bytes, stream=None, check=True) -> int:
+    return _enqueue("moe_experts_backward",
+                    (d_out, d_x, d_topk_w, workspace) +
+                    (tuple(getattr(grads, "keep", ())) if grads else ()),
+                    stream, check,
+                    ctypes.byref(p), ctypes.byref(saved), ptr(d_out),
+                    ctypes.byref(weights), ptr(d_x), ptr(d_topk_w),
+                    None if grads is None else ctypes.byref(grads),
+                    ptr(workspace), ws_bytes)
 
 
 # ------------------------------------------------- device weight plumbing

@@ -7,6 +7,8 @@
 
 #include "block.h"
 #include "common.h"
+#include "few.h"
+#include "train.h"
 
 using namespace moe;
 
@@ -796,6 +798,343 @@ moe_status moe_layer_forward_scored(
   }
   return layer_impl(p, logits, bias, x, w, l2p, replica_count, out,
                     expert_counts, workspace, ws_bytes, stream, nullptr, &sl);
+}
+
+// ------------------------------------------------------- a few tokens
+namespace {
+struct FewScratch {
+  int32_t* ids;
+  float* w;
+  FewList* list;
+  bf16_t* h;
+};
+FewScratch carve_few(Carver& c, const moe_problem* p) {
+  FewScratch f{};
+  f.ids = c.take<int32_t>((size_t)MOE_FEW_TOKENS * p->k);
+  f.w = c.take<float>((size_t)MOE_FEW_TOKENS * p->k);
+  f.list = c.take<FewList>(1);
+  f.h = c.take<bf16_t>((size_t)few_entries(p) * MOE_FEW_TOKENS * p->I);
+  return f;
+}
+moe_status check_few(const moe_problem* p) {
+  const moe_status st = moe_check_problem(p);
+  if (st != MOE_OK) return st;
+  return p->T > MOE_FEW_TOKENS || p->act_dtype != MOE_BF16 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+}  // namespace
+
+moe_status moe_layer_few_workspace_size(const moe_problem* p, size_t* bytes) {
+  const moe_status st = check_few(p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+  Carver c(nullptr);
+  carve_few(c, p);
+  *bytes = c.used;
+  return MOE_OK;
+}
+
+moe_status moe_layer_forward_few(const moe_problem* p, const moe_router* r,
+                                 const void* logits, const float* bias,
+                                 const void* x, const moe_weights* w,
+                                 const int32_t* l2p,
+                                 const int32_t* replica_count, void* out,
+                                 int32_t* expert_counts, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  moe_status st = check_few(p);
+  if (st != MOE_OK) return st;
+  if (r) {
+    if ((st = moe_check_router(r)) != MOE_OK) return st;
+    if (r->T != p->T || r->E != p->E || r->k != p->k) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  if ((st = check_map(p, l2p, replica_count)) != MOE_OK) return st;
+  if ((st = check_weights(p, w)) != MOE_OK) return st;
+  hipStream_t s = S(stream);
+  if (p->T == 0) {
+    if (expert_counts)
+      return hip_status(launch_fill_i32(expert_counts, 0, (size_t)p->E, s));
+    return MOE_OK;
+  }
+  if (!logits || !x || !out || !al16(x) || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
+  size_t need;
+  moe_layer_few_workspace_size(p, &need);
+  if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  Carver c(workspace);
+  const FewScratch f = carve_few(c, p);
+  FewCall call{};
+  call.x = (const bf16_t*)x;
+  call.weights = w;
+  call.l2p = l2p;
+  call.rep = replica_count;
+  call.counts = expert_counts;
+  call.list = f.list;
+  call.h = f.h;
+  call.out = out;
+  // a router inside the first kernel holds at most 256 experts
+  if (!r && p->E <= 256) {
+    call.logits = (const float*)logits;
+    call.bias = bias;
+  } else {
+    const hipError_t e =
+        r ? launch_route_scored(r, logits, bias, f.ids, f.w, nullptr, nullptr, s)
+          : launch_route_topk((const float*)logits, bias, p->T, p->E, p->k,
+                              f.ids, f.w, nullptr, s);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+    call.ids = f.ids;
+    call.w = f.w;
+  }
+  return hip_status(launch_few(p, call, s));
+}
+
+// --------------------------------------------------- 8-bit checkpoints
+moe_status moe_check_rows(const moe_rows* r) {
+  if (!r || r->rows < 0 || r->cols < 1 || r->stride < r->cols)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (r->dtype < MOE_F32 || r->dtype > MOE_FP8_E4M3) return MOE_ERR_INVALID_ARGUMENT;
+  if (r->dtype == MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+  // groups of 128 columns are counted in 32 bits
+  if ((double)r->rows * (((double)r->cols + 127.0) / 128.0) >= 2147483647.0)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_checkpoint_rows(const moe_rows* r, const void* src,
+                               uint8_t* codes, float* scales, void* stream) {
+  const moe_status st = moe_check_rows(r);
+  if (st != MOE_OK) return st;
+  if (r->rows == 0) return MOE_OK;
+  if (!src || !codes || !scales) return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(launch_checkpoint_rows(src, r->dtype, r->rows, r->cols,
+                                           r->stride, codes, scales, S(stream)));
+}
+
+moe_status moe_restore_rows(const moe_rows* r, const uint8_t* codes,
+                            const float* scales, void* dst, void* stream) {
+  const moe_status st = moe_check_rows(r);
+  if (st != MOE_OK) return st;
+  if (r->rows == 0) return MOE_OK;
+  if (!codes || !scales || !dst) return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(launch_restore_rows(codes, scales, r->rows, r->cols,
+                                        r->dtype, r->stride, dst, S(stream)));
+}
+
+// ------------------------------------------------ training the experts
+namespace {
+moe_status check_experts(const moe_problem* p) {
+  const moe_status st = moe_check_problem(p);
+  if (st != MOE_OK) return st;
+  return p->act_dtype != MOE_BF16 || p->weight_dtype != MOE_BF16
+             ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+bool saved_ok(const moe_saved* v) {
+  return v && v->offsets && v->row_token && v->row_weight && v->pair_row &&
+         v->x_codes && v->x_scales && v->gu_codes && v->gu_scales &&
+         al16(v->x_codes) && al16(v->gu_codes);
+}
+
+struct ExpertsScratch {
+  int4* tiles;
+  int32_t* tile_count;
+  // forward
+  DispatchScratch d;
+  float* gu;           // [rows][2 I]
+  bf16_t* h;           // [rows][I] (backward: the weighted h)
+  float* y;            // [cap][H] (backward: the rows' d_x)
+  float* y_shared;     // [T][H]
+  // backward
+  float* dh;           // [rows][I]
+  bf16_t* dgu;         // [rows][2 I]
+  bf16_t* x;           // [T][H]
+  float* d_row;        // [cap]
+};
+
+ExpertsScratch carve_experts(Carver& c, const moe_problem* p, bool backward) {
+  ExpertsScratch e{};
+  const size_t cap = (size_t)cap_rows(p), T = (size_t)p->T;
+  const size_t rows = cap + (p->has_shared ? T : 0);
+  // at most one tile per 16 rows (balanced tiles) and one per group
+  e.tiles = c.take<int4>((size_t)p->num_physical + 2 + (rows + 15) / 16);
+  e.tile_count = c.take<int32_t>(4);
+  e.h = c.take<bf16_t>(rows * p->I);
+  e.y = c.take<float>(cap * p->H);
+  if (p->has_shared) e.y_shared = c.take<float>(T * p->H);
+  if (backward) {
+    e.dh = c.take<float>(rows * p->I);
+    e.dgu = c.take<bf16_t>(rows * 2 * p->I);
+    e.x = c.take<bf16_t>(T * p->H);
+    e.d_row = c.take<float>(cap);
+  } else {
+    e.d = carve_dispatch(c, p);
+    e.gu = c.take<float>(rows * 2 * p->I);
+  }
+  return e;
+}
+
+size_t experts_need(const moe_problem* p, bool backward) {
+  Carver c(nullptr);
+  carve_experts(c, p, backward);
+  return c.used;
+}
+
+TrainGemm train_gemm(const moe_problem* p, const moe_weights* w,
+                     const ExpertsScratch& e) {
+  return {e.tiles, e.tile_count, p->num_physical, (int)cap_rows(p), p->T,
+          p->H, p->I, p->has_shared, w};
+}
+}  // namespace
+
+moe_status moe_experts_workspace_size(const moe_problem* p, size_t* bytes) {
+  const moe_status st = check_experts(p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+  *bytes = std::max(experts_need(p, false), experts_need(p, true));
+  return MOE_OK;
+}
+
+moe_status moe_experts_forward(const moe_problem* p, const void* x,
+                               const int32_t* topk_ids, const float* topk_w,
+                               const int32_t* l2p,
+                               const int32_t* replica_count,
+                               const moe_weights* w, const moe_saved* saved,
+                               void* out, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  moe_status st = check_experts(p);
+  if (st != MOE_OK) return st;
+  if ((st = check_map(p, l2p, replica_count)) != MOE_OK) return st;
+  if ((st = check_weights(p, w)) != MOE_OK) return st;
+  if (p->T == 0) return MOE_OK;
+  if (!x || !topk_ids || !topk_w || !out || !saved_ok(saved) || !al16(x) || !al16(out))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!workspace || ws_bytes < experts_need(p, false)) return MOE_ERR_WORKSPACE;
+  hipStream_t s = S(stream);
+  Carver c(workspace);
+  const ExpertsScratch e = carve_experts(c, p, false);
+  const int cap = (int)cap_rows(p);
+  DispatchExtras extras{};
+  extras.E = p->E;
+  extras.tiles = e.tiles;
+  extras.tile_count = e.tile_count;
+  extras.BM = gemm_tile_rows();
+  extras.balanced = 1;
+  extras.has_shared = p->has_shared;
+  st = dispatch_impl(p, x, topk_ids, topk_w, l2p, replica_count, nullptr,
+                     nullptr, saved->offsets, saved->row_token,
+                     saved->row_weight, saved->pair_row, e.d, s, nullptr,
+                     /*materialize=*/false, &extras);
+  if (st != MOE_OK) return st;
+  hipError_t h = launch_checkpoint_rows(x, MOE_BF16, p->T, p->H, p->H,
+                                        saved->x_codes, saved->x_scales, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  const TrainGemm g = train_gemm(p, w, e);
+  h = launch_gemm_gate_up(g, (const bf16_t*)x, saved->row_token, e.gu, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  const ExpertRows rows{saved->offsets + p->num_physical, cap, p->T,
+                        p->has_shared, p->I};
+  h = launch_swiglu_save(rows, e.gu, e.h, saved->gu_codes, saved->gu_scales, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  h = launch_gemm_down(g, e.h, e.y, e.y_shared, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  return hip_status(launch_combine(e.y, saved->pair_row, topk_w, e.y_shared,
+                                   p->T, p->H, p->k, p->out_dtype, out, s));
+}
+
+moe_status moe_experts_backward(const moe_problem* p, const moe_saved* saved,
+                                const void* d_out, const moe_weights* w,
+                                void* d_x, float* d_topk_w,
+                                const moe_weight_grads* grads, void* workspace,
+                                size_t ws_bytes, void* stream) {
+  moe_status st = check_experts(p);
+  if (st != MOE_OK) return st;
+  if ((st = check_weights(p, w)) != MOE_OK) return st;
+  if (!d_x && !d_topk_w && !grads) return MOE_ERR_INVALID_ARGUMENT;
+  if (grads) {
+    if (grads->dtype < MOE_F32 || grads->dtype > MOE_FP8_E4M3) return MOE_ERR_INVALID_ARGUMENT;
+    if (grads->dtype == MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+    const void* all[6] = {grads->d_gate, grads->d_up, grads->d_down,
+                          grads->sh_d_gate, grads->sh_d_up, grads->sh_d_down};
+    for (int i = 0; i < (p->has_shared ? 6 : 3); ++i)
+      if (!all[i] || !al16(all[i])) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  hipStream_t s = S(stream);
+  const size_t HI = (size_t)p->H * p->I;
+  if (p->T == 0) {
+    if (!grads) return MOE_OK;
+    const size_t words = HI * (grads->dtype == MOE_F32 ? 4 : 2) / 4;
+    void* routed[3] = {grads->d_gate, grads->d_up, grads->d_down};
+    void* shared[3] = {grads->sh_d_gate, grads->sh_d_up, grads->sh_d_down};
+    for (int i = 0; i < 3; ++i) {
+      if (launch_fill_i32((int32_t*)routed[i], 0, words * p->num_physical, s) != hipSuccess)
+        return MOE_ERR_HIP;
+      if (p->has_shared && launch_fill_i32((int32_t*)shared[i], 0, words, s) != hipSuccess)
+        return MOE_ERR_HIP;
+    }
+    return MOE_OK;
+  }
+  if (!d_out || !saved_ok(saved) || !al16(d_out) || !al16(d_x)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!workspace || ws_bytes < experts_need(p, true)) return MOE_ERR_WORKSPACE;
+  Carver c(workspace);
+  const ExpertsScratch e = carve_experts(c, p, true);
+  const int cap = (int)cap_rows(p), P = p->num_physical;
+  const bf16_t* d = (const bf16_t*)d_out;
+  hipError_t h = launch_build_tiles(saved->offsets, P, p->has_shared, p->T,
+                                    gemm_tile_rows(), 1, 0, e.tiles,
+                                    e.tile_count, 0, nullptr, nullptr, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  const TrainGemm g = train_gemm(p, w, e);
+  h = launch_gemm_down_back(g, d, saved->row_token, e.dh, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  const ExpertRows rows{saved->offsets + P, cap, p->T, p->has_shared, p->I};
+  h = launch_swiglu_backward(rows, e.dh, saved->gu_codes, saved->gu_scales,
+                             saved->row_weight, e.dgu, e.h, e.d_row, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  if (d_topk_w) {
+    h = launch_pair_gather(e.d_row, saved->pair_row, p->T * p->k, d_topk_w, s);
+    if (h != hipSuccess) return MOE_ERR_HIP;
+  }
+  if (d_x) {
+    h = launch_gemm_gate_up_back(g, e.dgu, e.y, e.y_shared, s);
+    if (h != hipSuccess) return MOE_ERR_HIP;
+    h = launch_combine(e.y, saved->pair_row, nullptr, e.y_shared, p->T, p->H,
+                       p->k, MOE_BF16, d_x, s);
+    if (h != hipSuccess) return MOE_ERR_HIP;
+  }
+  if (!grads) return MOE_OK;
+  h = launch_restore_rows(saved->x_codes, saved->x_scales, p->T, p->H,
+                          MOE_BF16, p->H, e.x, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  WeightGrad q{};
+  q.P = P;
+  q.T = p->T;
+  q.has_shared = p->has_shared;
+  q.cap = cap;
+  q.offsets = saved->offsets;
+  q.dtype = grads->dtype;
+  // d_W_gate and d_W_up: x^T (dg | du)
+  q.M = p->H;
+  q.N = 2 * p->I;
+  q.N0 = p->I;
+  q.a = e.x;
+  q.lda = p->H;
+  q.a_rows = saved->row_token;
+  q.b = e.dgu;
+  q.ldb = 2 * p->I;
+  q.out[0] = grads->d_gate;
+  q.out[1] = grads->d_up;
+  q.out_shared[0] = grads->sh_d_gate;
+  q.out_shared[1] = grads->sh_d_up;
+  if (launch_weight_grad(q, s) != hipSuccess) return MOE_ERR_HIP;
+  // d_W_down: (w h)^T d_out
+  q.M = p->I;
+  q.N = q.N0 = p->H;
+  q.a = e.h;
+  q.lda = p->I;
+  q.a_rows = nullptr;
+  q.b = d;
+  q.ldb = p->H;
+  q.b_rows = saved->row_token;
+  q.out[0] = grads->d_down;
+  q.out_shared[0] = grads->sh_d_down;
+  return hip_status(launch_weight_grad(q, s));
 }
 
 moe_status moe_prepack_weights(const void* src, int32_t K, int32_t N,

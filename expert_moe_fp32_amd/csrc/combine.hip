@@ -7,7 +7,8 @@
 // loads its columns of the shared expert's row; then each thread owns
 // groups of 4 columns, CPT groups per pass, and issues all of a pass's row
 // loads before it accumulates, in float32 and slot order, with one rounding
-// to the output type.
+// to the output type.  Without route weights every row counts once (the sum
+// of the rows' gradients over a token).
 #include "common.h"
 
 namespace moe {
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(256) void k_combine(
   if (threadIdx.x < 64) {     // lanes j < k load slot j; local slots keep order
     const int j = threadIdx.x;
     const int r = j < k ? pair_row[(size_t)t * k + j] : -1;
-    const float wj = j < k ? w[(size_t)t * k + j] : 0.0f;
+    const float wj = j < k ? (w ? w[(size_t)t * k + j] : 1.0f) : 0.0f;
     const uint64_t m = __ballot(r >= 0);
     if (r >= 0) {
       const int pos = __popcll(m & ((1ull << j) - 1ull));

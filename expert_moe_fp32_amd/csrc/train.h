@@ -1,0 +1,80 @@
+// Launch functions of the 8-bit checkpoints, of the experts' forward and
+// backward pass that use them, and of the layer for a few tokens.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+// rows of activations <-> E4M3 codes [T][C] and scales [T][ceil(C / 128)]
+hipError_t launch_checkpoint_rows(const void* src, int dtype, long T, int C,
+                                  long stride, uint8_t* codes, float* scales,
+                                  hipStream_t s);
+hipError_t launch_restore_rows(const uint8_t* codes, const float* scales,
+                               long T, int C, int dtype, long stride,
+                               void* dst, hipStream_t s);
+
+// Rows of the experts' intermediate arrays: routed ones [0, offsets[P]), the
+// shared expert's [cap, cap + T).
+struct ExpertRows {
+  const int32_t* n_routed;    // device: offsets + P
+  int cap, T, has_shared, I;
+};
+// gu [rows][2 I] float32 (gate, then up) -> h = silu(gate) * up in bf16, and
+// the checkpoint of gu
+hipError_t launch_swiglu_save(const ExpertRows& r, const float* gu, bf16_t* h,
+                              uint8_t* codes, float* scales, hipStream_t s);
+// Backward of it from the checkpoint: dh [rows][I] float32 (of the unweighted
+// output) -> dgu [rows][2 I] and the weighted h [rows][I] in bf16, and
+// d_pair[row] = sum_i dh h for routed rows.  row_weight: [cap].
+hipError_t launch_swiglu_backward(const ExpertRows& r, const float* dh,
+                                  const uint8_t* codes, const float* scales,
+                                  const float* row_weight, bf16_t* dgu,
+                                  bf16_t* hw, float* d_row, hipStream_t s);
+// d_topk_w[t][j] = d_row[pair_row[t][j]], 0 for a pair that is not local
+hipError_t launch_pair_gather(const float* d_row, const int32_t* pair_row,
+                              int n, float* d_topk_w, hipStream_t s);
+
+// The training GEMMs over a list of balanced tiles of up to gemm_tile_rows()
+// rows (see gemm_ring.h).
+struct TrainGemm {
+  const int4* tiles;
+  const int32_t* tile_count;
+  int P, cap, T, H, I, has_shared;
+  const moe_weights* w;
+};
+// out [rows][2 I] float32: x Wg, then x Wu, x gathered through a_rows
+hipError_t launch_gemm_gate_up(const TrainGemm& g, const bf16_t* x,
+                               const int32_t* a_rows, float* out,
+                               hipStream_t s);
+// y_routed [cap][H], y_shared [T][H] float32: h Wd
+hipError_t launch_gemm_down(const TrainGemm& g, const bf16_t* h,
+                            float* y_routed, float* y_shared, hipStream_t s);
+// out [rows][I] float32: d Wd^T, d [T][H] gathered through a_rows
+hipError_t launch_gemm_down_back(const TrainGemm& g, const bf16_t* d,
+                                 const int32_t* a_rows, float* out,
+                                 hipStream_t s);
+// dx_routed [cap][H], dx_shared [T][H] float32: dg Wg^T + du Wu^T
+hipError_t launch_gemm_gate_up_back(const TrainGemm& g, const bf16_t* dgu,
+                                    float* dx_routed, float* dx_shared,
+                                    hipStream_t s);
+
+// Weight gradients (gemm_wgrad.hip): for every group the product of its rows
+// of a, transposed, with its rows of b, written to out [M][N].
+struct WeightGrad {
+  int M, N;                   // columns of a and of b, multiples of 128
+  int P, T, has_shared, cap;
+  const int32_t* offsets;     // [P + 1]
+  const bf16_t* a;            // routed rows [rows][lda]; the shared group's
+  const bf16_t* b;            //   from row cap (or 0 where gathered)
+  long lda, ldb;
+  const int32_t* a_rows;      // routed rows through it ([T] rows), or null
+  const int32_t* b_rows;
+  void* out[2];               // [P][M][N0] and, for columns from N0 on, the
+  void* out_shared[2];        //   second; the shared group's
+  int N0;                     // columns of an output array (N or N / 2)
+  int dtype;                  // of the outputs
+};
+hipError_t launch_weight_grad(const WeightGrad& g, hipStream_t s);
+
+}  // namespace moe

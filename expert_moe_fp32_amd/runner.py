@@ -251,3 +251,65 @@ class DeviceLayer:
                          d_y_shared=None):
         return L.moe_combine_backward(self.p, d_out, b.y_perm, b.pair_row,
                                       b.w, d_y_perm, d_w, d_y_shared)
+
+    # ------------------------------------- a few tokens, and training
+    def forward_few(self, logits, bias, x, out, counts=None,
+                    router: Optional[L.Router] = None, ws=None):
+        """The layer for a few tokens; ``ws``: moe_layer_few_workspace_size
+        bytes (made here without it)."""
+        n = L.moe_layer_few_workspace_size(self.p)
+        if ws is None:
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return L.moe_layer_forward_few(
+            self.p, router, logits, bias, x, self.weights, self.l2p, self.rep,
+            out, counts, ws, ws.numel())
+
+    def train_buffers(self, grads="f32") -> "TrainBuffers":
+        p, dev = self.p, self.device
+        T, H, I, P = p.T, p.H, p.I, p.num_physical
+        cap = T * min(p.k, p.num_local)
+        rows = cap + (T if p.has_shared else 0)
+
+        def z(*shape, dt=torch.float32):
+            return torch.empty(shape, dtype=dt, device=dev)
+        saved = dict(
+            offsets=z(P + 1, dt=torch.int32), row_token=z(max(cap, 1), dt=torch.int32),
+            row_weight=z(max(cap, 1)), pair_row=z(max(T, 1), p.k, dt=torch.int32),
+            x_codes=z(max(T, 1), H, dt=torch.uint8), x_scales=z(max(T, 1), H // 128),
+            gu_codes=z(max(rows, 1), 2 * I, dt=torch.uint8),
+            gu_scales=z(max(rows, 1), 2 * I // 128))
+        dt = {"f32": torch.float32, "bf16": torch.bfloat16}[grads]
+        g = dict(d_gate=z(P, H, I, dt=dt), d_up=z(P, H, I, dt=dt),
+                 d_down=z(P, I, H, dt=dt))
+        if p.has_shared:
+            g.update(sh_gate=z(H, I, dt=dt), sh_up=z(H, I, dt=dt),
+                     sh_down=z(I, H, dt=dt))
+        out_dt = torch.float32 if p.out_dtype == L.MOE_F32 else torch.bfloat16
+        return TrainBuffers(
+            saved=saved, handle=L.make_saved(**saved),
+            out=z(max(T, 1), H, dt=out_dt),
+            d_x=z(max(T, 1), H, dt=torch.bfloat16), d_w=z(max(T, 1), p.k),
+            grads=g, grads_handle=L.make_weight_grads(dtype=grads, **g),
+            ws=z(L.moe_experts_workspace_size(p), dt=torch.uint8))
+
+    def experts_forward(self, b: "TrainBuffers", x, ids, w):
+        return L.moe_experts_forward(self.p, x, ids, w, self.l2p, self.rep,
+                                     self.weights, b.handle, b.out, b.ws,
+                                     b.ws.numel())
+
+    def experts_backward(self, b: "TrainBuffers", d_out):
+        return L.moe_experts_backward(self.p, b.handle, d_out, self.weights,
+                                      b.d_x, b.d_w, b.grads_handle, b.ws,
+                                      b.ws.numel())
+
+
+@dataclasses.dataclass
+class TrainBuffers:
+    saved: dict                # the arrays of moe_saved
+    handle: L.Saved
+    out: torch.Tensor
+    d_x: torch.Tensor
+    d_w: torch.Tensor
+    grads: dict                # the arrays of moe_weight_grads
+    grads_handle: L.WeightGrads
+    ws: torch.Tensor

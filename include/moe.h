@@ -472,6 +472,132 @@ MOE_API moe_status moe_layer_forward_scored(
     const void* pre_gain, void* out, void* resid_out, void* x_out,
     int32_t* expert_counts, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------ a few tokens
+ * The whole layer for up to MOE_FEW_TOKENS tokens (a few decoding sequences)
+ * in two kernels, or three where the router is a kernel of its own (scored
+ * routing, or more than 256 experts).  The same layer as moe_layer_forward
+ * (r NULL) or moe_layer_forward_scored without a norm (r given, with p's T, E
+ * and k), from the same weights, with
+ *   recipes  BF16 and FP8; FP8 weights are taken as the values that their
+ *            codes and block scales stand for, and the activations stay bf16
+ *            (moe_layer_forward quantises them); F32 is UNSUPPORTED
+ *   h        rounded to bf16, as in the BF16 recipe
+ *   sums     in float32; out rounded once
+ * Arguments as in the two; expert_counts may be NULL.  T = 0 clears it.
+ * UNSUPPORTED for T > MOE_FEW_TOKENS.  Identical inputs give identical
+ * outputs. */
+#define MOE_FEW_TOKENS 16
+MOE_API moe_status moe_layer_few_workspace_size(const moe_problem* p,
+                                                size_t* bytes);
+MOE_API moe_status moe_layer_forward_few(
+    const moe_problem* p, const moe_router* r, const void* logits,
+    const float* bias, const void* x, const moe_weights* w,
+    const int32_t* l2p, const int32_t* replica_count, void* out,
+    int32_t* expert_counts, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------ 8-bit checkpoints
+ * Activations kept for the backward pass as E4M3 codes.  128 neighbouring
+ * columns of a row (the last group of a row may be shorter) share a scale, the
+ * smallest power of two s with |v| / s <= 448 for the group's finite values:
+ * not below 2^-100, and 1 for a group of zeros.  A code is the E4M3 value
+ * nearest to v / s, ties to even; infinities and NaN become NaN; where s is
+ * 2^120, magnitudes stop at 240 s.  code * s is exact in bf16 and float32. */
+typedef struct {
+  int32_t rows;
+  int32_t cols;
+  int32_t dtype;   /* MOE_F32 or MOE_BF16 of the rows                         */
+  int64_t stride;  /* elements between rows, at least cols                    */
+} moe_rows;
+
+/* Validate a description of rows (host only). */
+MOE_API moe_status moe_check_rows(const moe_rows* r);
+
+/*   src    [rows][stride], the first cols of each row read
+ *   codes  [rows][cols] out
+ *   scales [rows][ceil(cols / 128)] float32 out
+ * and back:
+ *   dst    [rows][stride] out, the first cols of each row written; codes with
+ *          scales of any value are multiplied in float32 and rounded to dtype
+ * Any alignment of the element type; 16-byte aligned rows, codes at their
+ * pieces' alignment and cols a multiple of 8 are fastest. */
+MOE_API moe_status moe_checkpoint_rows(const moe_rows* r, const void* src,
+                                       uint8_t* codes, float* scales,
+                                       void* stream);
+MOE_API moe_status moe_restore_rows(const moe_rows* r, const uint8_t* codes,
+                                    const float* scales, void* dst,
+                                    void* stream);
+
+/* ------------------------------------------------ training the experts
+ * Everything of the layer past its router -- dispatch, experts, combine -- for
+ * a training step, BF16 recipe (others are UNSUPPORTED), and its gradients.
+ * The forward pass leaves what the backward needs: the permutation, and 8-bit
+ * checkpoints of the layer's input and of the experts' gate and up products.
+ * Intermediate rows: routed row r (r < offsets[P]) in row r, the shared
+ * expert's row of token t in row cap + t. */
+typedef struct {
+  int32_t* offsets;     /* [P + 1]                                            */
+  int32_t* row_token;   /* [cap]                                              */
+  float* row_weight;    /* [cap]                                              */
+  int32_t* pair_row;    /* [T][k]            (these four as in moe_dispatch)  */
+  uint8_t* x_codes;     /* [T][H]                                             */
+  float* x_scales;      /* [T][H / 128]                                       */
+  uint8_t* gu_codes;    /* [cap + T][2 I] gate, then up of a row (the T rows   */
+  float* gu_scales;     /* [cap + T][2 I / 128]       with has_shared only)   */
+} moe_saved;
+
+/* Bytes of scratch for the forward or the backward call (host only). */
+MOE_API moe_status moe_experts_workspace_size(const moe_problem* p,
+                                              size_t* bytes);
+
+/*   x        [T][H] bf16
+ *   topk_ids, topk_w  from moe_route_topk or moe_route_scored
+ *   saved    every array written (rows behind the last one untouched)
+ *   out      [T][H] out_dtype, as moe_layer_forward's: with unrounded gate and
+ *            up products, not the checkpoint's
+ * T = 0 writes nothing. */
+MOE_API moe_status moe_experts_forward(
+    const moe_problem* p, const void* x, const int32_t* topk_ids,
+    const float* topk_w, const int32_t* l2p, const int32_t* replica_count,
+    const moe_weights* w, const moe_saved* saved, void* out, void* workspace,
+    size_t ws_bytes, void* stream);
+
+/* Gradients of the experts' weights, in the logical layout; every element is
+ * written (an expert without rows gets zeros). */
+typedef struct {
+  void* d_gate;      /* [P][H][I], one after another by physical id           */
+  void* d_up;        /* [P][H][I]                                             */
+  void* d_down;      /* [P][I][H]                                             */
+  void* sh_d_gate;   /* [H][I], [H][I], [I][H] with has_shared, else ignored  */
+  void* sh_d_up;
+  void* sh_d_down;
+  int32_t dtype;     /* MOE_F32 or MOE_BF16 of all six                        */
+} moe_weight_grads;
+
+/* With g, u and x as the checkpoints hold them, q = sigmoid(g) and, for row r
+ * of token t with route weight w_r (1 for the shared expert):
+ *   e_r   = d_out[t] W_down^T                      (float32)
+ *   h     = g q u
+ *   d_topk_w[t][j] = sum_i e_r h  of pair (t, j)'s row, 0 for a pair that is
+ *                                 not local
+ *   dg    = w_r e_r u q (1 + g (1 - q)),  du = w_r e_r g q
+ *   d_x[t] = sum over the token's rows of dg W_gate^T + du W_up^T
+ *   d_W_gate = sum over the expert's rows of x[t]^T dg, d_W_up likewise,
+ *   d_W_down = sum of (w_r h)^T d_out[t]
+ * dg, du and w_r h are rounded to bf16 (the matrix cores' type); sums are
+ * float32, each in a fixed order, and outputs rounded once.
+ *   saved    as moe_experts_forward left it
+ *   d_out    [T][H] bf16
+ *   w        the forward's prepared weights
+ *   d_x      [T][H] bf16 out, or NULL
+ *   d_topk_w [T][k] float32 out, or NULL
+ *   grads    out, or NULL
+ * At least one output is given.  T = 0 clears the weights' gradients. */
+MOE_API moe_status moe_experts_backward(
+    const moe_problem* p, const moe_saved* saved, const void* d_out,
+    const moe_weights* w, void* d_x, float* d_topk_w,
+    const moe_weight_grads* grads, void* workspace, size_t ws_bytes,
+    void* stream);
+
 /* Profiling variant of moe_layer_forward: the same work, plus hipEventRecord
  * on `stream` at the stage boundaries, so a caller can time each stage with
  * hipEventElapsedTime.  events: HOST array of MOE_STAGE_EVENTS hipEvent_t

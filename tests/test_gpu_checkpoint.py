@@ -1,0 +1,123 @@
+"""8-bit checkpoints of rows on the GPU: codes and scales bit for bit, and
+back."""
+import numpy as np
+import pytest
+
+from oracle import train as ot
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(T, C, dtype, pad, seed, shift=0):
+    """Rows [T][C] of a wider array, `shift` elements into its memory."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, C + pad, generator=g) * torch.randn(
+        C + pad, generator=g).mul(2).exp()
+    x[T // 2] = 0.0
+    if C > 200:
+        x[0, 128:256] = 0.0
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    flat = torch.empty(T * (C + pad) + shift, dtype=dt, device="cuda")
+    v = flat[shift:].view(T, C + pad)
+    v.copy_(x.to(dt))
+    return v
+
+
+@pytest.mark.parametrize("T,C,dtype,pad,shift", [
+    (1, 1, "f32", 0, 0), (1, 1, "bf16", 0, 0), (3, 7, "bf16", 2, 1),
+    (5, 128, "bf16", 0, 0), (4, 127, "f32", 5, 0), (9, 129, "bf16", 0, 0),
+    (17, 256, "f32", 0, 1), (33, 1004, "bf16", 4, 0), (33, 1004, "f32", 4, 0),
+    (6, 2501, "f32", 3, 0), (6, 2501, "bf16", 0, 0), (40, 7168, "bf16", 8, 0),
+    (300, 7168, "bf16", 0, 0), (2200, 640, "f32", 0, 0),
+    (3000, 1001, "bf16", 0, 0), (1500, 1536, "bf16", 0, 3),
+])
+def test_codes_and_back(T, C, dtype, pad, shift):
+    import torch
+    import expert_moe_fp32_amd as m
+    print(T, C, dtype, pad, shift, flush=True)
+    x = rows_of(T, C, dtype, pad, T + C, shift)
+    n = -(-C // 128)
+    codes = torch.full((T + 1, C), 77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((T + 1, n), 7.0, device="cuda")
+    d = m.make_rows(T, C, dtype=dtype, stride=C + pad)
+    m.moe_checkpoint_rows(d, x, codes, scales)
+    torch.cuda.synchronize()
+    assert (codes[T] == 77).all() and (scales[T] == 7.0).all()
+    some = np.unique(np.r_[0, T // 2, T - 1, np.arange(0, T, max(1, T // 20))])
+    rc, rs = ot.checkpoint(x[some, :C].double().cpu().numpy())
+    assert np.array_equal(scales[:T].cpu().numpy()[some], rs)
+    assert np.array_equal(codes[:T].cpu().numpy()[some], rc)
+    # back: exactly code * scale, which both types hold
+    for to in ("f32", "bf16"):
+        dt = {"f32": torch.float32, "bf16": torch.bfloat16}[to]
+        y = torch.full((T + 1, C + pad), 9.0, dtype=dt, device="cuda")
+        m.moe_restore_rows(m.make_rows(T, C, dtype=to, stride=C + pad), codes,
+                           scales, y)
+        torch.cuda.synchronize()
+        v = codes[:T].view(torch.float8_e4m3fn).double()
+        v = v * scales[:T].double().repeat_interleave(128, 1)[:, :C]
+        assert torch.equal(y[:T, :C].double(), v)
+        assert (y[:T, C:] == 9.0).all() and (y[T] == 9.0).all()
+
+
+def test_what_is_not_finite_becomes_nan():
+    import torch
+    import expert_moe_fp32_amd as m
+    x = torch.randn(3, 256, device="cuda")
+    x[0, 3], x[0, 200], x[1, 5] = float("inf"), float("nan"), -float("inf")
+    x[2, :128] = float("nan")
+    codes = torch.empty(3, 256, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(3, 2, device="cuda")
+    m.moe_checkpoint_rows(m.make_rows(3, 256, dtype="f32"), x, codes, scales)
+    y = torch.empty_like(x)
+    m.moe_restore_rows(m.make_rows(3, 256, dtype="f32"), codes, scales, y)
+    torch.cuda.synchronize()
+    rc, rs = ot.checkpoint(x.double().cpu().numpy())
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    want = ot.values(rc, rs)
+    assert np.array_equal(y.double().cpu().numpy(), want, equal_nan=True)
+    assert np.isnan(want).sum() == 131
+
+
+def test_the_ends_of_the_range():
+    """Magnitudes from the smallest to the largest of float32, powers of two
+    and the scales' borders among them."""
+    import torch
+    import expert_moe_fp32_amd as m
+    top = torch.finfo(torch.float32).max
+    sizes = [top, 2.0 ** 127, 448.0, np.nextafter(np.float32(448.0), np.float32(500.0)),
+             449.0, 256.0, 224.0, 1.75, 1.0, 1e-3, 2.0 ** -90, 2.0 ** -100,
+             2.0 ** -115, 1e-38, 1e-45]
+    x = torch.zeros(len(sizes), 128)
+    g = torch.Generator().manual_seed(1)
+    for i, s in enumerate(sizes):
+        x[i] = torch.rand(128, generator=g) * 2 - 1
+        x[i] *= s
+        x[i, 7], x[i, 11] = float(s), -float(s)
+    x = x.cuda()
+    codes = torch.empty(len(sizes), 128, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(len(sizes), 1, device="cuda")
+    m.moe_checkpoint_rows(m.make_rows(len(sizes), 128, dtype="f32"), x, codes,
+                          scales)
+    torch.cuda.synchronize()
+    rc, rs = ot.checkpoint(x.double().cpu().numpy())
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    assert np.array_equal(codes.cpu().numpy(), rc)
+
+
+def test_scales_of_any_value_are_rounded_once():
+    import torch
+    import expert_moe_fp32_amd as m
+    g = torch.Generator().manual_seed(2)
+    codes = torch.randint(0, 127, (20, 300), generator=g, dtype=torch.uint8).cuda()
+    scales = torch.rand(20, 3, generator=g).cuda()
+    for to, half in (("f32", 2.0 ** -24), ("bf16", 2.0 ** -8)):
+        dt = {"f32": torch.float32, "bf16": torch.bfloat16}[to]
+        y = torch.empty(20, 300, dtype=dt, device="cuda")
+        m.moe_restore_rows(m.make_rows(20, 300, dtype=to), codes, scales, y)
+        torch.cuda.synchronize()
+        v = codes.view(torch.float8_e4m3fn).double() * \
+            scales.double().repeat_interleave(128, 1)[:, :300]
+        # one product in float32, then the rounding to the type
+        assert ((y.double() - v).abs() <= (half + 2.0 ** -24) * v.abs()).all()
