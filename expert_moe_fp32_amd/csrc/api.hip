@@ -939,12 +939,12 @@ struct ExpertsScratch {
   DispatchScratch d;
   float* gu;           // [rows][2 I]
   bf16_t* h;           // [rows][I] (backward: the weighted h)
-  float* y;            // [cap][H] (backward: the rows' d_x)
-  float* y_shared;     // [T][H]
+  float* y;            // [cap][H] (backward: the rows' d_x, then their x and
+                       // d_out in bf16)
+  float* y_shared;     // [T][H]   (backward: likewise)
   // backward
   float* dh;           // [rows][I]
   bf16_t* dgu;         // [rows][2 I]
-  bf16_t* x;           // [T][H]
   float* d_row;        // [cap]
 };
 
@@ -961,7 +961,6 @@ ExpertsScratch carve_experts(Carver& c, const moe_problem* p, bool backward) {
   if (backward) {
     e.dh = c.take<float>(rows * p->I);
     e.dgu = c.take<bf16_t>(rows * 2 * p->I);
-    e.x = c.take<bf16_t>(T * p->H);
     e.d_row = c.take<float>(cap);
   } else {
     e.d = carve_dispatch(c, p);
@@ -1099,41 +1098,31 @@ moe_status moe_experts_backward(const moe_problem* p, const moe_saved* saved,
     if (h != hipSuccess) return MOE_ERR_HIP;
   }
   if (!grads) return MOE_OK;
-  h = launch_restore_rows(saved->x_codes, saved->x_scales, p->T, p->H,
-                          MOE_BF16, p->H, e.x, s);
+  // the rows of both products' operands side by side, in the place of the
+  // rows' d_x, which nobody needs any more
+  const int H = p->H, I = p->I;
+  bf16_t* xr = (bf16_t*)e.y;
+  bf16_t* dr = xr + (size_t)cap * H;
+  h = launch_gather_pair(saved->x_codes, saved->x_scales, d, saved->row_token,
+                         rows.n_routed, cap, H, xr, dr, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
+  bf16_t* xs = (bf16_t*)e.y_shared;
+  if (p->has_shared) {
+    h = launch_restore_rows(saved->x_codes, saved->x_scales, p->T, H, MOE_BF16, H, xs, s);
+    if (h != hipSuccess) return MOE_ERR_HIP;
+  }
   WeightGrad q{};
   q.P = P;
   q.T = p->T;
   q.has_shared = p->has_shared;
-  q.cap = cap;
   q.offsets = saved->offsets;
   q.dtype = grads->dtype;
-  // d_W_gate and d_W_up: x^T (dg | du)
-  q.M = p->H;
-  q.N = 2 * p->I;
-  q.N0 = p->I;
-  q.a = e.x;
-  q.lda = p->H;
-  q.a_rows = saved->row_token;
-  q.b = e.dgu;
-  q.ldb = 2 * p->I;
-  q.out[0] = grads->d_gate;
-  q.out[1] = grads->d_up;
-  q.out_shared[0] = grads->sh_d_gate;
-  q.out_shared[1] = grads->sh_d_up;
-  if (launch_weight_grad(q, s) != hipSuccess) return MOE_ERR_HIP;
-  // d_W_down: (w h)^T d_out
-  q.M = p->I;
-  q.N = q.N0 = p->H;
-  q.a = e.h;
-  q.lda = p->I;
-  q.a_rows = nullptr;
-  q.b = d;
-  q.ldb = p->H;
-  q.b_rows = saved->row_token;
-  q.out[0] = grads->d_down;
-  q.out_shared[0] = grads->sh_d_down;
+  // d_W_gate and d_W_up: x^T (dg | du); d_W_down: (w h)^T d_out
+  q.product[0] = {H, 2 * I, I, xr, e.dgu, xs, e.dgu + (size_t)cap * 2 * I, H, 2 * I,
+                  {grads->d_gate, grads->d_up},
+                  {grads->sh_d_gate, grads->sh_d_up}};
+  q.product[1] = {I, H, H, e.h, dr, e.h + (size_t)cap * I, d, I, H,
+                  {grads->d_down, nullptr}, {grads->sh_d_down, nullptr}};
   return hip_status(launch_weight_grad(q, s));
 }
 

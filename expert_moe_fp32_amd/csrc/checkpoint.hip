@@ -344,6 +344,39 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(
   }
 }
 
+// Sixteen columns a thread: 16 bytes of codes, twice 16 bytes of d and of each
+// output.
+__global__ __launch_bounds__(256) void k_gather_pair(
+    const uint8_t* __restrict__ codes, const float* __restrict__ scales,
+    const bf16_t* __restrict__ d, const int32_t* __restrict__ row_token,
+    const int32_t* __restrict__ n_rows, int C, bf16_t* __restrict__ x_out,
+    bf16_t* __restrict__ d_out) {
+  const uint32_t per_row = (uint32_t)C / 16;
+  const long count = (long)*n_rows * per_row;
+  for (long q = (long)blockIdx.x * 256 + threadIdx.x; q < count;
+       q += (long)gridDim.x * 256) {
+    const uint32_t r = (uint32_t)(q / per_row), c = (uint32_t)(q - (long)r * per_row) * 16;
+    const long t = row_token[r];
+    const u32x4_t code = *(const u32x4_t*)(codes + t * C + c);
+    const float s = scales[t * (C / 128) + (c >> 7)];
+    const u32x4_t d0 = *(const u32x4_t*)(d + t * C + c);
+    const u32x4_t d1 = *(const u32x4_t*)(d + t * C + c + 8);
+    u32x4_t o[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[4];
+      code_values(code[i], v);
+      o[i >> 1][2 * (i & 1)] = pack_bf16(v[0] * s, v[1] * s);
+      o[i >> 1][2 * (i & 1) + 1] = pack_bf16(v[2] * s, v[3] * s);
+    }
+    const size_t at = (size_t)r * C + c;
+    *(u32x4_t*)(x_out + at) = o[0];
+    *(u32x4_t*)(x_out + at + 8) = o[1];
+    *(u32x4_t*)(d_out + at) = d0;
+    *(u32x4_t*)(d_out + at + 8) = d1;
+  }
+}
+
 __global__ __launch_bounds__(256) void k_pair_gather(
     const float* __restrict__ d_row, const int32_t* __restrict__ pair_row,
     int n, float* __restrict__ d_topk_w) {
@@ -387,6 +420,16 @@ hipError_t launch_swiglu_backward(const ExpertRows& r, const float* dh,
   const long most = (long)r.cap + (r.has_shared ? r.T : 0);
   k_swiglu_backward<<<(unsigned)(most < 4096 ? most : 4096), 256, 0, s>>>(
       r, dh, codes, scales, row_weight, dgu, hw, d_row);
+  return hipGetLastError();
+}
+
+hipError_t launch_gather_pair(const uint8_t* codes, const float* scales,
+                              const bf16_t* d, const int32_t* row_token,
+                              const int32_t* n_rows, int cap, int C,
+                              bf16_t* x_out, bf16_t* d_out, hipStream_t s) {
+  const long most = ((long)cap * (C / 16) + 255) / 256;
+  k_gather_pair<<<(unsigned)(most < 8192 ? most : 8192), 256, 0, s>>>(
+      codes, scales, d, row_token, n_rows, C, x_out, d_out);
   return hipGetLastError();
 }
 

@@ -13,6 +13,13 @@ hipError_t launch_checkpoint_rows(const void* src, int dtype, long T, int C,
 hipError_t launch_restore_rows(const uint8_t* codes, const float* scales,
                                long T, int C, int dtype, long stride,
                                void* dst, hipStream_t s);
+// Rows in the order of an index: x_out[r] = the values of codes[row_token[r]]
+// and d_out[r] = d[row_token[r]], bf16, for r < *n_rows (at most cap); C a
+// multiple of 128
+hipError_t launch_gather_pair(const uint8_t* codes, const float* scales,
+                              const bf16_t* d, const int32_t* row_token,
+                              const int32_t* n_rows, int cap, int C,
+                              bf16_t* x_out, bf16_t* d_out, hipStream_t s);
 
 // Rows of the experts' intermediate arrays: routed ones [0, offsets[P]), the
 // shared expert's [cap, cap + T).
@@ -59,21 +66,24 @@ hipError_t launch_gemm_gate_up_back(const TrainGemm& g, const bf16_t* dgu,
                                     float* dx_routed, float* dx_shared,
                                     hipStream_t s);
 
-// Weight gradients (gemm_wgrad.hip): for every group the product of its rows
-// of a, transposed, with its rows of b, written to out [M][N].
-struct WeightGrad {
-  int M, N;                   // columns of a and of b, multiples of 128
-  int P, T, has_shared, cap;
-  const int32_t* offsets;     // [P + 1]
-  const bf16_t* a;            // routed rows [rows][lda]; the shared group's
-  const bf16_t* b;            //   from row cap (or 0 where gathered)
+// Weight gradients (gemm_wgrad.hip): for every group of rows and product, a^T b
+// over the group's rows, written to [M][N0] arrays: columns [0, N0) of b to
+// out[0], the others to out[1].
+struct WeightProduct {
+  int M, N, N0;               // columns of a and of b, of an output; multiples of 128
+  const bf16_t* a;            // routed rows, in order
+  const bf16_t* b;
+  const bf16_t* a_shared;     // the shared group's
+  const bf16_t* b_shared;
   long lda, ldb;
-  const int32_t* a_rows;      // routed rows through it ([T] rows), or null
-  const int32_t* b_rows;
-  void* out[2];               // [P][M][N0] and, for columns from N0 on, the
-  void* out_shared[2];        //   second; the shared group's
-  int N0;                     // columns of an output array (N or N / 2)
+  void* out[2];               // [P][M][N0]
+  void* out_shared[2];        // the shared group's
+};
+struct WeightGrad {
+  int P, T, has_shared;
+  const int32_t* offsets;     // [P + 1]
   int dtype;                  // of the outputs
+  WeightProduct product[2];
 };
 hipError_t launch_weight_grad(const WeightGrad& g, hipStream_t s);
 
