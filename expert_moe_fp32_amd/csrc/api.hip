@@ -945,7 +945,6 @@ struct ExpertsScratch {
   // backward
   float* dh;           // [rows][I]
   bf16_t* dgu;         // [rows][2 I]
-  float* d_row;        // [cap]
 };
 
 ExpertsScratch carve_experts(Carver& c, const moe_problem* p, bool backward) {
@@ -961,7 +960,6 @@ ExpertsScratch carve_experts(Carver& c, const moe_problem* p, bool backward) {
   if (backward) {
     e.dh = c.take<float>(rows * p->I);
     e.dgu = c.take<bf16_t>(rows * 2 * p->I);
-    e.d_row = c.take<float>(cap);
   } else {
     e.d = carve_dispatch(c, p);
     e.gu = c.take<float>(rows * 2 * p->I);
@@ -1011,18 +1009,25 @@ moe_status moe_experts_forward(const moe_problem* p, const void* x,
   const int cap = (int)cap_rows(p);
   DispatchExtras extras{};
   extras.E = p->E;
-  extras.tiles = e.tiles;
-  extras.tile_count = e.tile_count;
-  extras.BM = gemm_tile_rows();
-  extras.balanced = 1;
-  extras.has_shared = p->has_shared;
+  // with a shared expert its tiles go among the others, by a kernel of its own
+  if (!p->has_shared) {
+    extras.tiles = e.tiles;
+    extras.tile_count = e.tile_count;
+    extras.BM = gemm_tile_rows();
+    extras.balanced = 1;
+  }
   st = dispatch_impl(p, x, topk_ids, topk_w, l2p, replica_count, nullptr,
                      nullptr, saved->offsets, saved->row_token,
                      saved->row_weight, saved->pair_row, e.d, s, nullptr,
                      /*materialize=*/false, &extras);
   if (st != MOE_OK) return st;
-  hipError_t h = launch_checkpoint_rows(x, MOE_BF16, p->T, p->H, p->H,
-                                        saved->x_codes, saved->x_scales, s);
+  hipError_t h = hipSuccess;
+  if (p->has_shared)
+    h = launch_train_tiles(saved->offsets, p->num_physical, 1, p->T,
+                           gemm_tile_rows(), e.tiles, e.tile_count, s);
+  if (h != hipSuccess) return MOE_ERR_HIP;
+  h = launch_checkpoint_rows(x, MOE_BF16, p->T, p->H, p->H, saved->x_codes,
+                             saved->x_scales, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   const TrainGemm g = train_gemm(p, w, e);
   h = launch_gemm_gate_up(g, (const bf16_t*)x, saved->row_token, e.gu, s);
@@ -1075,21 +1080,17 @@ moe_status moe_experts_backward(const moe_problem* p, const moe_saved* saved,
   const ExpertsScratch e = carve_experts(c, p, true);
   const int cap = (int)cap_rows(p), P = p->num_physical;
   const bf16_t* d = (const bf16_t*)d_out;
-  hipError_t h = launch_build_tiles(saved->offsets, P, p->has_shared, p->T,
-                                    gemm_tile_rows(), 1, 0, e.tiles,
-                                    e.tile_count, 0, nullptr, nullptr, s);
+  hipError_t h = launch_train_tiles(saved->offsets, P, p->has_shared, p->T,
+                                    gemm_tile_rows(), e.tiles, e.tile_count, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   const TrainGemm g = train_gemm(p, w, e);
   h = launch_gemm_down_back(g, d, saved->row_token, e.dh, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   const ExpertRows rows{saved->offsets + P, cap, p->T, p->has_shared, p->I};
-  h = launch_swiglu_backward(rows, e.dh, saved->gu_codes, saved->gu_scales,
-                             saved->row_weight, e.dgu, e.h, e.d_row, s);
+  const PairRows pairs{saved->row_token, saved->row_weight, saved->pair_row, p->k};
+  h = launch_swiglu_backward(rows, pairs, e.dh, saved->gu_codes,
+                             saved->gu_scales, e.dgu, e.h, d_topk_w, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
-  if (d_topk_w) {
-    h = launch_pair_gather(e.d_row, saved->pair_row, p->T * p->k, d_topk_w, s);
-    if (h != hipSuccess) return MOE_ERR_HIP;
-  }
   if (d_x) {
     h = launch_gemm_gate_up_back(g, e.dgu, e.y, e.y_shared, s);
     if (h != hipSuccess) return MOE_ERR_HIP;
@@ -1103,14 +1104,10 @@ moe_status moe_experts_backward(const moe_problem* p, const moe_saved* saved,
   const int H = p->H, I = p->I;
   bf16_t* xr = (bf16_t*)e.y;
   bf16_t* dr = xr + (size_t)cap * H;
+  bf16_t* xs = (bf16_t*)e.y_shared;      // (null without a shared expert)
   h = launch_gather_pair(saved->x_codes, saved->x_scales, d, saved->row_token,
-                         rows.n_routed, cap, H, xr, dr, s);
+                         rows.n_routed, cap, p->T, H, xr, dr, xs, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
-  bf16_t* xs = (bf16_t*)e.y_shared;
-  if (p->has_shared) {
-    h = launch_restore_rows(saved->x_codes, saved->x_scales, p->T, H, MOE_BF16, H, xs, s);
-    if (h != hipSuccess) return MOE_ERR_HIP;
-  }
   WeightGrad q{};
   q.P = P;
   q.T = p->T;

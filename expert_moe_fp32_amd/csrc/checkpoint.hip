@@ -284,10 +284,15 @@ __global__ __launch_bounds__(256) void k_swiglu_save(
 // times the row's route weight w; the weight's own gradient sums dh h over
 // the row, per thread in column order, then over the threads.
 __global__ __launch_bounds__(256) void k_swiglu_backward(
-    ExpertRows r, const float* __restrict__ dh,
+    ExpertRows r, PairRows pr, const float* __restrict__ dh,
     const uint8_t* __restrict__ codes, const float* __restrict__ scales,
-    const float* __restrict__ row_weight, bf16_t* __restrict__ dgu,
-    bf16_t* __restrict__ hw, float* __restrict__ d_row) {
+    bf16_t* __restrict__ dgu, bf16_t* __restrict__ hw,
+    float* __restrict__ d_topk_w) {
+  if (d_topk_w) {                                // pairs without a row
+    const int pairs = r.T * pr.k;
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < pairs; i += gridDim.x * 256)
+      if (pr.pair_row[i] < 0) d_topk_w[i] = 0.0f;
+  }
   __shared__ float part[2][4];
   const int I = r.I, blocks = I / 128;
   const int n = *r.n_routed + (r.has_shared ? r.T : 0);
@@ -295,7 +300,7 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(
   for (int i = blockIdx.x; i < n; i += gridDim.x, turn ^= 1) {
     const long row = intermediate_row(r, i);
     const bool routed = row < r.cap && i < *r.n_routed;
-    const float w = routed ? row_weight[row] : 1.0f;
+    const float w = routed ? pr.row_weight[row] : 1.0f;
     float sum = 0.0f;
     for (int c = threadIdx.x * 8; c < I; c += 256 * 8) {
       const long at = row * 2 * I + c;
@@ -334,13 +339,19 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(
       *(u32x4_t*)(dgu + at + I) = ou;
       *(u32x4_t*)(hw + row * I + c) = oh;
     }
-    if (!routed) continue;                       // uniform for the workgroup
+    if (!routed || !d_topk_w) continue;          // uniform for the workgroup
+    // (the slot whose row this is)
+    long pair = -1;
+    if ((int)threadIdx.x < pr.k) {
+      pair = (long)pr.row_token[row] * pr.k + threadIdx.x;
+      if (pr.pair_row[pair] != row) pair = -1;
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
     if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = sum;
     __syncthreads();                             // (two buffers: one barrier a row)
-    if (threadIdx.x == 0)
-      d_row[row] = (part[turn][0] + part[turn][1]) + (part[turn][2] + part[turn][3]);
+    if (pair >= 0)
+      d_topk_w[pair] = (part[turn][0] + part[turn][1]) + (part[turn][2] + part[turn][3]);
   }
 }
 
@@ -349,19 +360,24 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(
 __global__ __launch_bounds__(256) void k_gather_pair(
     const uint8_t* __restrict__ codes, const float* __restrict__ scales,
     const bf16_t* __restrict__ d, const int32_t* __restrict__ row_token,
-    const int32_t* __restrict__ n_rows, int C, bf16_t* __restrict__ x_out,
-    bf16_t* __restrict__ d_out) {
+    const int32_t* __restrict__ n_rows, int T, int C,
+    bf16_t* __restrict__ x_out, bf16_t* __restrict__ d_out,
+    bf16_t* __restrict__ x_all) {
   const uint32_t per_row = (uint32_t)C / 16;
-  const long count = (long)*n_rows * per_row;
+  const int n = *n_rows;
+  const long count = ((long)n + (x_all ? T : 0)) * per_row;
   for (long q = (long)blockIdx.x * 256 + threadIdx.x; q < count;
        q += (long)gridDim.x * 256) {
     const uint32_t r = (uint32_t)(q / per_row), c = (uint32_t)(q - (long)r * per_row) * 16;
-    const long t = row_token[r];
+    const bool routed = r < (uint32_t)n;
+    const long t = routed ? row_token[r] : (int)(r - n);
     const u32x4_t code = *(const u32x4_t*)(codes + t * C + c);
     const float s = scales[t * (C / 128) + (c >> 7)];
-    const u32x4_t d0 = *(const u32x4_t*)(d + t * C + c);
-    const u32x4_t d1 = *(const u32x4_t*)(d + t * C + c + 8);
-    u32x4_t o[2];
+    u32x4_t d0, d1, o[2];
+    if (routed) {
+      d0 = *(const u32x4_t*)(d + t * C + c);
+      d1 = *(const u32x4_t*)(d + t * C + c + 8);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float v[4];
@@ -370,20 +386,14 @@ __global__ __launch_bounds__(256) void k_gather_pair(
       o[i >> 1][2 * (i & 1) + 1] = pack_bf16(v[2] * s, v[3] * s);
     }
     const size_t at = (size_t)r * C + c;
-    *(u32x4_t*)(x_out + at) = o[0];
-    *(u32x4_t*)(x_out + at + 8) = o[1];
-    *(u32x4_t*)(d_out + at) = d0;
-    *(u32x4_t*)(d_out + at + 8) = d1;
+    bf16_t* x = routed ? x_out + at : x_all + t * C + c;
+    *(u32x4_t*)x = o[0];
+    *(u32x4_t*)(x + 8) = o[1];
+    if (routed) {
+      *(u32x4_t*)(d_out + at) = d0;
+      *(u32x4_t*)(d_out + at + 8) = d1;
+    }
   }
-}
-
-__global__ __launch_bounds__(256) void k_pair_gather(
-    const float* __restrict__ d_row, const int32_t* __restrict__ pair_row,
-    int n, float* __restrict__ d_topk_w) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int row = pair_row[i];
-  d_topk_w[i] = row >= 0 ? d_row[row] : 0.0f;
 }
 
 }  // namespace
@@ -413,29 +423,24 @@ hipError_t launch_swiglu_save(const ExpertRows& r, const float* gu, bf16_t* h,
   return hipGetLastError();
 }
 
-hipError_t launch_swiglu_backward(const ExpertRows& r, const float* dh,
-                                  const uint8_t* codes, const float* scales,
-                                  const float* row_weight, bf16_t* dgu,
-                                  bf16_t* hw, float* d_row, hipStream_t s) {
+hipError_t launch_swiglu_backward(const ExpertRows& r, const PairRows& p,
+                                  const float* dh, const uint8_t* codes,
+                                  const float* scales, bf16_t* dgu, bf16_t* hw,
+                                  float* d_topk_w, hipStream_t s) {
   const long most = (long)r.cap + (r.has_shared ? r.T : 0);
   k_swiglu_backward<<<(unsigned)(most < 4096 ? most : 4096), 256, 0, s>>>(
-      r, dh, codes, scales, row_weight, dgu, hw, d_row);
+      r, p, dh, codes, scales, dgu, hw, d_topk_w);
   return hipGetLastError();
 }
 
 hipError_t launch_gather_pair(const uint8_t* codes, const float* scales,
                               const bf16_t* d, const int32_t* row_token,
-                              const int32_t* n_rows, int cap, int C,
-                              bf16_t* x_out, bf16_t* d_out, hipStream_t s) {
-  const long most = ((long)cap * (C / 16) + 255) / 256;
+                              const int32_t* n_rows, int cap, int T, int C,
+                              bf16_t* x_out, bf16_t* d_out, bf16_t* x_all,
+                              hipStream_t s) {
+  const long most = (((long)cap + (x_all ? T : 0)) * (C / 16) + 255) / 256;
   k_gather_pair<<<(unsigned)(most < 8192 ? most : 8192), 256, 0, s>>>(
-      codes, scales, d, row_token, n_rows, C, x_out, d_out);
-  return hipGetLastError();
-}
-
-hipError_t launch_pair_gather(const float* d_row, const int32_t* pair_row,
-                              int n, float* d_topk_w, hipStream_t s) {
-  k_pair_gather<<<(n + 255) / 256, 256, 0, s>>>(d_row, pair_row, n, d_topk_w);
+      codes, scales, d, row_token, n_rows, T, C, x_out, d_out, x_all);
   return hipGetLastError();
 }
 

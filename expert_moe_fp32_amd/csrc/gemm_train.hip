@@ -34,7 +34,51 @@ hipError_t launch(GArgs& a, int columns, int chunk, hipStream_t s) {
 
 constexpr int kColumns = 32 * kGemmTN * kGemmWN;       // of a tile's B
 
+// One workgroup, a thread a group.  Tiles of routed groups wait for their
+// weights where an expert has some hundred rows, the shared expert's for the
+// matrix cores: side by side they fill each other's gaps.  Routed tile r goes
+// to place r + floor(r S / R), shared tile j to j + ceil((j + 1) R / S), of R
+// and S of them.
+__global__ __launch_bounds__(1024) void k_train_tiles(
+    const int32_t* __restrict__ offsets, int P, int has_shared, int T, int BM,
+    int4* __restrict__ tiles, int32_t* __restrict__ count) {
+  __shared__ int32_t wave_sum[16];
+  const int g = threadIdx.x, lane = g & 63, wv = g >> 6;
+  const int start = g < P ? offsets[g] : 0;
+  const int rows = g < P ? offsets[g + 1] - start : 0;
+  int per = 1, sper = 1;
+  const int n = tile_split(rows, BM, 1, &per);
+  const int S = has_shared ? tile_split(T, BM, 1, &sper) : 0;
+  int upto = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(upto, d, 64);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) wave_sum[wv] = upto;
+  __syncthreads();
+  int before = upto - n, R = 0;
+  for (int v = 0; v < 16; ++v) {
+    if (v < wv) before += wave_sum[v];
+    R += wave_sum[v];
+  }
+  for (int i = 0; i < n; ++i) {
+    const long r = before + i;
+    tiles[r + (R > 0 ? r * S / R : 0)] = make_int4(g, start + i * per, min(per, rows - i * per), 0);
+  }
+  for (int j = g; j < S; j += 1024)
+    tiles[j + ((long)(j + 1) * R + S - 1) / S] = make_int4(P, j * sper, min(sper, T - j * sper), 0);
+  if (g == 0) count[0] = R + S;
+}
+
 }  // namespace
+
+hipError_t launch_train_tiles(const int32_t* offsets, int P, int has_shared,
+                              int T, int BM, int4* tiles, int32_t* count,
+                              hipStream_t s) {
+  k_train_tiles<<<1, 1024, 0, s>>>(offsets, P, has_shared, T, BM, tiles, count);
+  return hipGetLastError();
+}
 
 hipError_t launch_gemm_gate_up(const TrainGemm& g, const bf16_t* x,
                                const int32_t* a_rows, float* out,

@@ -13,13 +13,14 @@ hipError_t launch_checkpoint_rows(const void* src, int dtype, long T, int C,
 hipError_t launch_restore_rows(const uint8_t* codes, const float* scales,
                                long T, int C, int dtype, long stride,
                                void* dst, hipStream_t s);
-// Rows in the order of an index: x_out[r] = the values of codes[row_token[r]]
-// and d_out[r] = d[row_token[r]], bf16, for r < *n_rows (at most cap); C a
-// multiple of 128
+// Rows of checkpointed x [T][C] and of d [T][C], bf16, C a multiple of 128:
+// x_out[r] = x[row_token[r]] and d_out[r] = d[row_token[r]] for r < *n_rows (at
+// most cap), and x_all[t] = x[t] unless null
 hipError_t launch_gather_pair(const uint8_t* codes, const float* scales,
                               const bf16_t* d, const int32_t* row_token,
-                              const int32_t* n_rows, int cap, int C,
-                              bf16_t* x_out, bf16_t* d_out, hipStream_t s);
+                              const int32_t* n_rows, int cap, int T, int C,
+                              bf16_t* x_out, bf16_t* d_out, bf16_t* x_all,
+                              hipStream_t s);
 
 // Rows of the experts' intermediate arrays: routed ones [0, offsets[P]), the
 // shared expert's [cap, cap + T).
@@ -32,18 +33,26 @@ struct ExpertRows {
 hipError_t launch_swiglu_save(const ExpertRows& r, const float* gu, bf16_t* h,
                               uint8_t* codes, float* scales, hipStream_t s);
 // Backward of it from the checkpoint: dh [rows][I] float32 (of the unweighted
-// output) -> dgu [rows][2 I] and the weighted h [rows][I] in bf16, and
-// d_pair[row] = sum_i dh h for routed rows.  row_weight: [cap].
-hipError_t launch_swiglu_backward(const ExpertRows& r, const float* dh,
-                                  const uint8_t* codes, const float* scales,
-                                  const float* row_weight, bf16_t* dgu,
-                                  bf16_t* hw, float* d_row, hipStream_t s);
-// d_topk_w[t][j] = d_row[pair_row[t][j]], 0 for a pair that is not local
-hipError_t launch_pair_gather(const float* d_row, const int32_t* pair_row,
-                              int n, float* d_topk_w, hipStream_t s);
+// output) -> dgu [rows][2 I] and the weighted h [rows][I] in bf16, and (unless
+// null) d_topk_w [T][k]: sum_i dh h of a pair's row, 0 for one that is not
+// local.
+struct PairRows {
+  const int32_t* row_token;   // [cap]
+  const float* row_weight;    // [cap]
+  const int32_t* pair_row;    // [T][k]
+  int k;
+};
+hipError_t launch_swiglu_backward(const ExpertRows& r, const PairRows& p,
+                                  const float* dh, const uint8_t* codes,
+                                  const float* scales, bf16_t* dgu, bf16_t* hw,
+                                  float* d_topk_w, hipStream_t s);
 
-// The training GEMMs over a list of balanced tiles of up to gemm_tile_rows()
-// rows (see gemm_ring.h).
+// The tile list of the training GEMMs: balanced tiles of up to BM rows, the
+// shared expert's spread evenly among the routed ones.
+hipError_t launch_train_tiles(const int32_t* offsets, int P, int has_shared,
+                              int T, int BM, int4* tiles, int32_t* count,
+                              hipStream_t s);
+// The training GEMMs over that list (see gemm_ring.h).
 struct TrainGemm {
   const int4* tiles;
   const int32_t* tile_count;
