@@ -975,7 +975,7 @@ size_t experts_need(const moe_problem* p, bool backward) {
 
 TrainGemm train_gemm(const moe_problem* p, const moe_weights* w,
                      const ExpertsScratch& e) {
-  return {e.tiles, e.tile_count, p->num_physical, (int)cap_rows(p), p->T,
+  return {train_tile_rows(p), e.tiles, e.tile_count, p->num_physical, (int)cap_rows(p), p->T,
           p->H, p->I, p->has_shared, w};
 }
 }  // namespace
@@ -1013,7 +1013,7 @@ moe_status moe_experts_forward(const moe_problem* p, const void* x,
   if (!p->has_shared) {
     extras.tiles = e.tiles;
     extras.tile_count = e.tile_count;
-    extras.BM = gemm_tile_rows();
+    extras.BM = train_tile_rows(p);
     extras.balanced = 1;
   }
   st = dispatch_impl(p, x, topk_ids, topk_w, l2p, replica_count, nullptr,
@@ -1024,7 +1024,7 @@ moe_status moe_experts_forward(const moe_problem* p, const void* x,
   hipError_t h = hipSuccess;
   if (p->has_shared)
     h = launch_train_tiles(saved->offsets, p->num_physical, 1, p->T,
-                           gemm_tile_rows(), e.tiles, e.tile_count, s);
+                           train_tile_rows(p), e.tiles, e.tile_count, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   h = launch_checkpoint_rows(x, MOE_BF16, p->T, p->H, p->H, saved->x_codes,
                              saved->x_scales, s);
@@ -1081,7 +1081,7 @@ moe_status moe_experts_backward(const moe_problem* p, const moe_saved* saved,
   const int cap = (int)cap_rows(p), P = p->num_physical;
   const bf16_t* d = (const bf16_t*)d_out;
   hipError_t h = launch_train_tiles(saved->offsets, P, p->has_shared, p->T,
-                                    gemm_tile_rows(), e.tiles, e.tile_count, s);
+                                    train_tile_rows(p), e.tiles, e.tile_count, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   const TrainGemm g = train_gemm(p, w, e);
   h = launch_gemm_down_back(g, d, saved->row_token, e.dh, s);

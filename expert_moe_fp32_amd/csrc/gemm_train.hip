@@ -4,6 +4,9 @@
 // the weight's output channels, 16 of which are the rows of a packed block,
 // so its operand comes out of LDS transposed (ds_read_b64_tr_b16) and no
 // second copy of the weights is laid out.
+#include <algorithm>
+#include <cmath>
+
 #include "gemm_ring.h"
 #include "train.h"
 
@@ -22,8 +25,133 @@ GArgs args(const TrainGemm& g, int K, int N) {
   return a;
 }
 
+// Small passes, whose 256 x 256 tiles would not fill the GPU and whose time is
+// the latency of their stages: 64 rows x 64 columns of B (G_PAIR: 32 of gate
+// and 32 of up) from four wavefronts of 32 x 32, stages of 128 of the
+// reduction (32 KiB), four in LDS, three in flight.  509 tokens of 1024 x 512,
+// 2 of 16 experts each: gate/up 18.8 us, down 11.4, gradients back through
+// each 15; the ring on 256 x 256 tiles 23.7, 14.5 and 23.9, the ring on 64 x
+// 128 tiles (stages of 32) 25.4, 15.4 and 29.
+constexpr int kSmallRows = 64, kSmallColumns = 64;
+
 template <int MODE>
-hipError_t launch(GArgs& a, int columns, int chunk, hipStream_t s) {
+__global__ __launch_bounds__(256) void k_gemm_small(GArgs a) {
+  // a stage: 64 rows of 256 bytes, their 16 chunks at chunk ^ (row % 16), then
+  // the weight's 16 packed blocks
+  __shared__ u32x4_t l0[2048], l1[2048], l2[2048], l3[2048];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w >> 1, wn = w & 1;
+  const int c16 = lane & 15, c32 = lane & 31, hi = (lane >> 4) & 1, ks = lane >> 5;
+  const int K = a.K, N = a.N, KT = K / 128;
+  const int total = a.tile_count[0] * a.nb_per_tile;
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    const int tile = item / a.nb_per_tile, nb = item - tile * a.nb_per_tile;
+    const int4 td = a.tiles[tile];
+    const int g = td.x, row0 = td.y, nrows = td.z;
+    const bool sh = g == a.P;
+    const char* W0 = (const char*)(sh ? a.w0_sh : a.w0_arr[g]);
+    const char* W1 = a.w1_arr ? (const char*)(sh ? a.w1_sh : a.w1_arr[g]) : W0;
+    // a transfer moves four rows of A (lane: row lane / 16, chunk slot lane %
+    // 16), or one block of the weight
+    const char* arow[4];
+    const char* block[4];
+    const char* block1[4];               // G_BACK: of the reduction's second half
+    const int half = MODE == G_BACK && a.w1_arr ? KT / 2 : KT;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int x = w + 4 * h, r = 4 * x + (lane >> 4);
+      const int rr = row0 + (r < nrows ? r : 0);       // (padded rows: unused)
+      const size_t src = sh ? rr : (a.a_rows ? a.a_rows[rr] : rr);
+      arow[h] = (const char*)(sh ? a.a_shared : a.a_routed) + src * K * 2 + ((c16 ^ (r & 15)) * 16);
+      block1[h] = nullptr;
+      if (MODE == G_BACK) {              // block x: 16 of the reduction, 32 columns
+        const size_t at = ((size_t)(x >> 1) * (N / 32) + nb * 2 + (x & 1)) * 1024 + lane * 16;
+        block[h] = W0 + at;
+        block1[h] = W1 + at - (size_t)half * N * 256;
+      } else {                           // 16 columns, 32 of the reduction
+        const int col = x >> 2;
+        const char* W = MODE == G_PAIR && col >= 2 ? W1 : W0;
+        const int n16 = MODE == G_PAIR ? nb * 2 + (col & 1) : nb * 4 + col;
+        block[h] = W + ((size_t)n16 * (K / 32) + (x & 3)) * 1024 + lane * 16;
+      }
+    }
+    auto issue = [&](int kt, u32x4_t* L) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        lds_dma16(arow[h] + (size_t)kt * 256, L + (w + 4 * h) * 64);
+        const char* b = MODE != G_BACK ? block[h] + (size_t)kt * 4096
+                        : (kt < half ? block[h] : block1[h]) + (size_t)kt * N * 256;
+        lds_dma16(b, L + 1024 + (w + 4 * h) * 64);
+      }
+    };
+    f32x16_t acc = {};
+    const int row = wm * 32 + c32;
+    const int tr = ((8 * ks + (c16 >> 2)) + 16 * (2 * hi + ((c16 >> 1) & 1))) * 16 +
+                   (c16 & 1) * 8 + 16384 + wn * 1024;
+    auto multiply = [&](const u32x4_t* L) {
+      u32x4_t fa[8], fb[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        fa[s] = L[row * 16 + ((2 * s + ks) ^ (row & 15))];
+        if constexpr (MODE == G_BACK) {
+          const u32x2g_t lo = lds_read_tr(L, tr + s * 2048);
+          const u32x2g_t up = lds_read_tr(L, tr + s * 2048 + 64);
+          fb[s] = u32x4_t{lo.x, lo.y, up.x, up.y};
+        } else {
+          fb[s] = L[1024 + ((2 * wn + hi) * 4 + (s >> 1)) * 64 + c16 + 16 * (2 * (s & 1) + ks)];
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) acc = mfma32b(fa[s], fb[s], acc);
+    };
+    lds_barrier();                       // the previous item is done with the ring
+    const int last = KT - 1;
+    issue(0, l0);
+    issue(min(1, last), l1);
+    issue(min(2, last), l2);
+    // stage k: wait for this wavefront's part (16 younger transfers), barrier
+    // (stage k complete, stage k - 1's slot free), fetch stage k + 3
+#define SMALL_STEP(S, L, NEXT)                                               \
+    if (kt + S < KT) {                                                       \
+      WAIT_VMCNT(16);                                                        \
+      lds_barrier();                                                         \
+      issue(min(kt + S + 3, last), NEXT);                                    \
+      multiply(L);                                                           \
+    }
+    for (int kt = 0; kt < KT; kt += 4) {
+      SMALL_STEP(0, l0, l3)
+      SMALL_STEP(1, l1, l0)
+      SMALL_STEP(2, l2, l1)
+      SMALL_STEP(3, l3, l2)
+    }
+#undef SMALL_STEP
+    WAIT_VMCNT(0);                       // the trailing re-reads have landed
+    // lane: column c32, rows 8 (r / 4) + 4 ks + r % 4
+    float* y;
+    int ld = N;
+    if (MODE == G_PAIR) {
+      ld = 2 * N;
+      y = a.y_routed + ((size_t)(sh ? a.cap : 0) + row0) * ld + wn * N + nb * 32 + c32;
+    } else {
+      y = (sh ? a.y_shared : a.y_routed) + (size_t)row0 * ld + nb * 64 + wn * 32 + c32;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int at = wm * 32 + 8 * (r >> 2) + 4 * ks + (r & 3);
+      if (at < nrows) y[(size_t)at * ld] = acc[r];
+    }
+  }
+}
+
+// `share`: outputs a column block has, of the columns of its B (G_PAIR: half)
+template <int MODE>
+hipError_t launch(const TrainGemm& g, GArgs& a, int share, int chunk, hipStream_t s) {
+  if (g.tile_rows == kSmallRows) {
+    a.nb_per_tile = a.N * share / kSmallColumns;
+    k_gemm_small<MODE><<<256, 256, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int columns = 32 * kGemmTN * kGemmWN / share;
   a.nb_per_tile = (a.N + columns - 1) / columns;
   a.chunk_cols = chunk_cols(a.nb_per_tile, chunk);
   // persistent: one workgroup per CU (128 KiB of LDS)
@@ -32,13 +160,13 @@ hipError_t launch(GArgs& a, int columns, int chunk, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int kColumns = 32 * kGemmTN * kGemmWN;       // of a tile's B
-
 // One workgroup, a thread a group.  Tiles of routed groups wait for their
 // weights where an expert has some hundred rows, the shared expert's for the
 // matrix cores: side by side they fill each other's gaps.  Routed tile r goes
 // to place r + floor(r S / R), shared tile j to j + ceil((j + 1) R / S), of R
-// and S of them.
+// and S of them.  Gate/up, down and d_x of 4096 tokens of 7168 x 2048, 32 of
+// 256 experts: 576, 349 and 498 us; the routed tiles first 590, 370 and 509,
+// the shared first 603, 364 and 519.
 __global__ __launch_bounds__(1024) void k_train_tiles(
     const int32_t* __restrict__ offsets, int P, int has_shared, int T, int BM,
     int4* __restrict__ tiles, int32_t* __restrict__ count) {
@@ -73,6 +201,20 @@ __global__ __launch_bounds__(1024) void k_train_tiles(
 
 }  // namespace
 
+// Small tiles where the gate and up products are up to 16 of their stages a CU
+// (tiles of evenly loaded groups x columns x reduction).  Whole passes on small
+// and on 256 x 256 tiles, forward and backward, us: 16 experts of 1024 x 512,
+// 1021 tokens (16 stages) 67 and 86 against 74 and 99, 2039 tokens (32) 100
+// and 125 against 93 and 125; of 2048 x 1024, 509 tokens (32) 104 and 162
+// against 98 and 161, 2039 tokens (128) 245 and 316 against 146 and 237.
+int train_tile_rows(const moe_problem* p) {
+  const double pairs = (double)p->T * p->k * p->num_local / p->E;
+  const double groups = std::max(1.0, std::min((double)p->num_physical, pairs));
+  const double tiles = groups * std::ceil(pairs / groups / kSmallRows) +
+                       (p->has_shared ? std::ceil((double)p->T / kSmallRows) : 0.0);
+  return tiles * (2.0 * p->I / kSmallColumns) * (p->H / 128) <= 16.0 * 256 ? kSmallRows : kGemmRows;
+}
+
 hipError_t launch_train_tiles(const int32_t* offsets, int P, int has_shared,
                               int T, int BM, int4* tiles, int32_t* count,
                               hipStream_t s) {
@@ -91,7 +233,7 @@ hipError_t launch_gemm_gate_up(const TrainGemm& g, const bf16_t* x,
   a.w0_sh = g.w->sh_gate;
   a.w1_sh = g.w->sh_up;
   a.y_routed = out;
-  return launch<G_PAIR>(a, kColumns / 2, 8, s);
+  return launch<G_PAIR>(g, a, 2, 8, s);
 }
 
 hipError_t launch_gemm_down(const TrainGemm& g, const bf16_t* h,
@@ -103,8 +245,7 @@ hipError_t launch_gemm_down(const TrainGemm& g, const bf16_t* h,
   a.w0_sh = g.w->sh_down;
   a.y_routed = y_routed;
   a.y_shared = y_shared;
-  if (a.N % kColumns == 0) return launch<G_DOWN>(a, kColumns, 4, s);
-  return launch<G_DOWN_ANY>(a, kColumns, 4, s);
+  return launch<G_DOWN_ANY>(g, a, 1, 4, s);
 }
 
 hipError_t launch_gemm_down_back(const TrainGemm& g, const bf16_t* d,
@@ -117,7 +258,7 @@ hipError_t launch_gemm_down_back(const TrainGemm& g, const bf16_t* d,
   a.w0_sh = g.w->sh_down;
   a.y_routed = out;
   a.y_shared = out + (size_t)g.cap * g.I;
-  return launch<G_BACK>(a, kColumns, 8, s);
+  return launch<G_BACK>(g, a, 1, 8, s);
 }
 
 hipError_t launch_gemm_gate_up_back(const TrainGemm& g, const bf16_t* dgu,
@@ -132,7 +273,7 @@ hipError_t launch_gemm_gate_up_back(const TrainGemm& g, const bf16_t* dgu,
   a.w1_sh = g.w->sh_up;
   a.y_routed = dx_routed;
   a.y_shared = dx_shared;
-  return launch<G_BACK>(a, kColumns, 4, s);
+  return launch<G_BACK>(g, a, 1, 4, s);
 }
 
 }  // namespace moe

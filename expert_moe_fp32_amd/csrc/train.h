@@ -47,6 +47,8 @@ hipError_t launch_swiglu_backward(const ExpertRows& r, const PairRows& p,
                                   const float* scales, bf16_t* dgu, bf16_t* hw,
                                   float* d_topk_w, hipStream_t s);
 
+// Rows of the training GEMMs' tiles: 256, in small passes 64 (gemm_train.hip).
+int train_tile_rows(const moe_problem* p);
 // The tile list of the training GEMMs: balanced tiles of up to BM rows, the
 // shared expert's spread evenly among the routed ones.
 hipError_t launch_train_tiles(const int32_t* offsets, int P, int has_shared,
@@ -54,6 +56,7 @@ hipError_t launch_train_tiles(const int32_t* offsets, int P, int has_shared,
                               hipStream_t s);
 // The training GEMMs over that list (see gemm_ring.h).
 struct TrainGemm {
+  int tile_rows;              // train_tile_rows
   const int4* tiles;
   const int32_t* tile_count;
   int P, cap, T, H, I, has_shared;

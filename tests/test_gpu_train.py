@@ -236,6 +236,18 @@ def test_against_the_oracle(kw, grads):
     check_step(Step(make_workload("prefill", seed=201, **kw), grads))
 
 
+LARGE = [
+    (dict(T=1500, H=768, I=640, E=8, num_local=8, k=2, shared=True), "f32"),
+    (dict(T=2000, H=640, I=896, E=3, num_local=2, k=2, shared=False), "bf16"),
+]
+
+
+@pytest.mark.parametrize("kw,grads", LARGE, ids=str)
+def test_on_large_tiles(kw, grads):
+    print(kw, grads, flush=True)
+    check_step(Step(make_workload("prefill", seed=211, **kw), grads))
+
+
 def test_a_share_in_the_middle_and_replicas():
     wl = make_workload("prefill", seed=202, T=70, H=256, I=128, E=16,
                        num_local=8, k=4, shared=True)
