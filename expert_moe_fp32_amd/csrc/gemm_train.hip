@@ -27,22 +27,23 @@ GArgs args(const TrainGemm& g, int K, int N) {
 
 // Small passes, whose 256 x 256 tiles would not fill the GPU and whose time is
 // the latency of their stages: 64 rows x 64 columns of B (G_PAIR: 32 of gate
-// and 32 of up) from four wavefronts of 32 x 32, stages of 128 of the
-// reduction (32 KiB), four in LDS, three in flight.  509 tokens of 1024 x 512,
-// 2 of 16 experts each: gate/up 18.8 us, down 11.4, gradients back through
-// each 15; the ring on 256 x 256 tiles 23.7, 14.5 and 23.9, the ring on 64 x
-// 128 tiles (stages of 32) 25.4, 15.4 and 29.
+// and 32 of up) from four wavefronts of 32 x 32, stages of 64 of the reduction
+// (16 KiB), four in LDS and one in registers, two workgroups a CU.  509 tokens
+// of 1024 x 512, 2 of 16 experts each: gate/up 14.2 us, down 10.1, gradients
+// back through each 13.1; stages of 128, one workgroup a CU 18.8, 11.4 and 15;
+// the ring on 256 x 256 tiles 23.7, 14.5 and 23.9, on 64 x 128 tiles (stages
+// of 32) 25.4, 15.4 and 29.
 constexpr int kSmallRows = 64, kSmallColumns = 64;
 
 template <int MODE>
-__global__ __launch_bounds__(256) void k_gemm_small(GArgs a) {
-  // a stage: 64 rows of 256 bytes, their 16 chunks at chunk ^ (row % 16), then
-  // the weight's 16 packed blocks
-  __shared__ u32x4_t l0[2048], l1[2048], l2[2048], l3[2048];
+__global__ __launch_bounds__(256, 2) void k_gemm_small(GArgs a) {
+  // a stage: 64 rows of 128 bytes, their 8 chunks at chunk ^ (row % 8), then
+  // the weight's 8 packed blocks
+  __shared__ u32x4_t l0[1024], l1[1024], l2[1024], l3[1024];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w >> 1, wn = w & 1;
   const int c16 = lane & 15, c32 = lane & 31, hi = (lane >> 4) & 1, ks = lane >> 5;
-  const int K = a.K, N = a.N, KT = K / 128;
+  const int K = a.K, N = a.N, KT = K / 64;
   const int total = a.tile_count[0] * a.nb_per_tile;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     const int tile = item / a.nb_per_tile, nb = item - tile * a.nb_per_tile;
@@ -51,78 +52,89 @@ __global__ __launch_bounds__(256) void k_gemm_small(GArgs a) {
     const bool sh = g == a.P;
     const char* W0 = (const char*)(sh ? a.w0_sh : a.w0_arr[g]);
     const char* W1 = a.w1_arr ? (const char*)(sh ? a.w1_sh : a.w1_arr[g]) : W0;
-    // a transfer moves four rows of A (lane: row lane / 16, chunk slot lane %
-    // 16), or one block of the weight
-    const char* arow[4];
-    const char* block[4];
-    const char* block1[4];               // G_BACK: of the reduction's second half
+    // a transfer moves eight rows of A (lane: row lane / 8, chunk slot lane %
+    // 8), or one block of the weight
+    const char* arow[2];
+    const char* block[2];
+    const char* block1[2];               // G_BACK: of the reduction's second half
     const int half = MODE == G_BACK && a.w1_arr ? KT / 2 : KT;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int x = w + 4 * h, r = 4 * x + (lane >> 4);
+    for (int h = 0; h < 2; ++h) {
+      const int x = w + 4 * h, r = 8 * x + (lane >> 3);
       const int rr = row0 + (r < nrows ? r : 0);       // (padded rows: unused)
       const size_t src = sh ? rr : (a.a_rows ? a.a_rows[rr] : rr);
-      arow[h] = (const char*)(sh ? a.a_shared : a.a_routed) + src * K * 2 + ((c16 ^ (r & 15)) * 16);
+      arow[h] = (const char*)(sh ? a.a_shared : a.a_routed) + src * K * 2 + (((lane ^ r) & 7) * 16);
       block1[h] = nullptr;
       if (MODE == G_BACK) {              // block x: 16 of the reduction, 32 columns
         const size_t at = ((size_t)(x >> 1) * (N / 32) + nb * 2 + (x & 1)) * 1024 + lane * 16;
         block[h] = W0 + at;
-        block1[h] = W1 + at - (size_t)half * N * 256;
+        block1[h] = W1 + at - (size_t)half * N * 128;
       } else {                           // 16 columns, 32 of the reduction
-        const int col = x >> 2;
+        const int col = x >> 1;
         const char* W = MODE == G_PAIR && col >= 2 ? W1 : W0;
         const int n16 = MODE == G_PAIR ? nb * 2 + (col & 1) : nb * 4 + col;
-        block[h] = W + ((size_t)n16 * (K / 32) + (x & 3)) * 1024 + lane * 16;
+        block[h] = W + ((size_t)n16 * (K / 32) + (x & 1)) * 1024 + lane * 16;
       }
     }
     auto issue = [&](int kt, u32x4_t* L) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        lds_dma16(arow[h] + (size_t)kt * 256, L + (w + 4 * h) * 64);
-        const char* b = MODE != G_BACK ? block[h] + (size_t)kt * 4096
-                        : (kt < half ? block[h] : block1[h]) + (size_t)kt * N * 256;
-        lds_dma16(b, L + 1024 + (w + 4 * h) * 64);
+      for (int h = 0; h < 2; ++h) {
+        lds_dma16(arow[h] + (size_t)kt * 128, L + (w + 4 * h) * 64);
+        const char* b = MODE != G_BACK ? block[h] + (size_t)kt * 2048
+                        : (kt < half ? block[h] : block1[h]) + (size_t)kt * N * 128;
+        lds_dma16(b, L + 512 + (w + 4 * h) * 64);
       }
     };
     f32x16_t acc = {};
     const int row = wm * 32 + c32;
     const int tr = ((8 * ks + (c16 >> 2)) + 16 * (2 * hi + ((c16 >> 1) & 1))) * 16 +
-                   (c16 & 1) * 8 + 16384 + wn * 1024;
-    auto multiply = [&](const u32x4_t* L) {
-      u32x4_t fa[8], fb[8];
+                   (c16 & 1) * 8 + 8192 + wn * 1024;
+    auto load = [&](const u32x4_t* L, u32x4_t (&fa)[4], u32x4_t (&fb)[4]) {
+      int t = tr;
+      asm volatile("" : "+v"(t));
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        fa[s] = L[row * 16 + ((2 * s + ks) ^ (row & 15))];
+      for (int s = 0; s < 4; ++s) {
+        fa[s] = L[row * 8 + ((2 * s + ks) ^ (row & 7))];
         if constexpr (MODE == G_BACK) {
-          const u32x2g_t lo = lds_read_tr(L, tr + s * 2048);
-          const u32x2g_t up = lds_read_tr(L, tr + s * 2048 + 64);
+          const u32x2g_t lo = lds_read_tr(L, t + s * 2048);
+          const u32x2g_t up = lds_read_tr(L, t + s * 2048 + 64);
           fb[s] = u32x4_t{lo.x, lo.y, up.x, up.y};
         } else {
-          fb[s] = L[1024 + ((2 * wn + hi) * 4 + (s >> 1)) * 64 + c16 + 16 * (2 * (s & 1) + ks)];
+          fb[s] = L[512 + ((2 * wn + hi) * 2 + (s >> 1)) * 64 + c16 + 16 * (2 * (s & 1) + ks)];
         }
       }
-#pragma unroll
-      for (int s = 0; s < 8; ++s) acc = mfma32b(fa[s], fb[s], acc);
     };
     lds_barrier();                       // the previous item is done with the ring
     const int last = KT - 1;
     issue(0, l0);
     issue(min(1, last), l1);
     issue(min(2, last), l2);
-    // stage k: wait for this wavefront's part (16 younger transfers), barrier
-    // (stage k complete, stage k - 1's slot free), fetch stage k + 3
-#define SMALL_STEP(S, L, NEXT)                                               \
-    if (kt + S < KT) {                                                       \
-      WAIT_VMCNT(16);                                                        \
+    issue(min(3, last), l3);
+    u32x4_t fa0[4], fb0[4], fa1[4], fb1[4];
+    WAIT_VMCNT(12);
+    lds_barrier();
+    load(l0, fa0, fb0);
+    // step k: wait for this wavefront's part of stage k + 1 (8 younger
+    // transfers), barrier (stage k + 1 complete, stage k read), fetch stage
+    // k + 4 into stage k's slot, read stage k + 1, multiply stage k.  Past the
+    // end the last stage is fetched and read again, and goes unused.
+#define SMALL_STEP(S, L, NEXT, A, B, NA, NB)                                 \
+    {                                                                        \
+      WAIT_VMCNT(8);                                                         \
       lds_barrier();                                                         \
-      issue(min(kt + S + 3, last), NEXT);                                    \
-      multiply(L);                                                           \
+      issue(min(kt + S + 4, last), L);                                       \
+      load(NEXT, NA, NB);                                                    \
+      __builtin_amdgcn_sched_barrier(0);                                     \
+      if (S < 2 || kt + S < KT)                                              \
+        for (int s = 0; s < 4; ++s) acc = mfma32b(A[s], B[s], acc);          \
     }
+    // (KT is even.  A way out of the loop in its middle would cost the
+    // compiler the knowledge of which slot is read, and it would wait for all.)
     for (int kt = 0; kt < KT; kt += 4) {
-      SMALL_STEP(0, l0, l3)
-      SMALL_STEP(1, l1, l0)
-      SMALL_STEP(2, l2, l1)
-      SMALL_STEP(3, l3, l2)
+      SMALL_STEP(0, l0, l1, fa0, fb0, fa1, fb1)
+      SMALL_STEP(1, l1, l2, fa1, fb1, fa0, fb0)
+      SMALL_STEP(2, l2, l3, fa0, fb0, fa1, fb1)
+      SMALL_STEP(3, l3, l0, fa1, fb1, fa0, fb0)
     }
 #undef SMALL_STEP
     WAIT_VMCNT(0);                       // the trailing re-reads have landed
@@ -148,7 +160,7 @@ template <int MODE>
 hipError_t launch(const TrainGemm& g, GArgs& a, int share, int chunk, hipStream_t s) {
   if (g.tile_rows == kSmallRows) {
     a.nb_per_tile = a.N * share / kSmallColumns;
-    k_gemm_small<MODE><<<256, 256, 0, s>>>(a);
+    k_gemm_small<MODE><<<512, 256, 0, s>>>(a);
     return hipGetLastError();
   }
   const int columns = 32 * kGemmTN * kGemmWN / share;
@@ -201,18 +213,19 @@ __global__ __launch_bounds__(1024) void k_train_tiles(
 
 }  // namespace
 
-// Small tiles where the gate and up products are up to 16 of their stages a CU
+// Small tiles where the gate and up products are up to 96 of their stages a CU
 // (tiles of evenly loaded groups x columns x reduction).  Whole passes on small
 // and on 256 x 256 tiles, forward and backward, us: 16 experts of 1024 x 512,
-// 1021 tokens (16 stages) 67 and 86 against 74 and 99, 2039 tokens (32) 100
-// and 125 against 93 and 125; of 2048 x 1024, 509 tokens (32) 104 and 162
-// against 98 and 161, 2039 tokens (128) 245 and 316 against 146 and 237.
+// 2 a token, 1021 tokens (32 stages) 56 and 75 against 74 and 99, 2039 tokens
+// (64) 82 and 108 against 96 and 125, 4093 tokens (128) 125 and 177 against
+// 110 and 163; of 2048 x 1024, 509 tokens (64) 81 and 136 against 98 and 158,
+// 2039 tokens (256) 182 and 262 against 147 and 238.
 int train_tile_rows(const moe_problem* p) {
   const double pairs = (double)p->T * p->k * p->num_local / p->E;
   const double groups = std::max(1.0, std::min((double)p->num_physical, pairs));
   const double tiles = groups * std::ceil(pairs / groups / kSmallRows) +
                        (p->has_shared ? std::ceil((double)p->T / kSmallRows) : 0.0);
-  return tiles * (2.0 * p->I / kSmallColumns) * (p->H / 128) <= 16.0 * 256 ? kSmallRows : kGemmRows;
+  return tiles * (2.0 * p->I / kSmallColumns) * (p->H / 64) <= 96.0 * 256 ? kSmallRows : kGemmRows;
 }
 
 hipError_t launch_train_tiles(const int32_t* offsets, int P, int has_shared,

@@ -239,6 +239,8 @@ def test_against_the_oracle(kw, grads):
 LARGE = [
     (dict(T=1500, H=768, I=640, E=8, num_local=8, k=2, shared=True), "f32"),
     (dict(T=2000, H=640, I=896, E=3, num_local=2, k=2, shared=False), "bf16"),
+    (dict(T=2500, H=768, I=640, E=8, num_local=8, k=2, shared=True), "bf16"),
+    (dict(T=4500, H=640, I=896, E=3, num_local=2, k=2, shared=False), "f32"),
 ]
 
 
