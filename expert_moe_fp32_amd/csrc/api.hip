@@ -1026,15 +1026,14 @@ moe_status moe_experts_forward(const moe_problem* p, const void* x,
     h = launch_train_tiles(saved->offsets, p->num_physical, 1, p->T,
                            train_tile_rows(p), e.tiles, e.tile_count, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
-  h = launch_checkpoint_rows(x, MOE_BF16, p->T, p->H, p->H, saved->x_codes,
-                             saved->x_scales, s);
-  if (h != hipSuccess) return MOE_ERR_HIP;
   const TrainGemm g = train_gemm(p, w, e);
   h = launch_gemm_gate_up(g, (const bf16_t*)x, saved->row_token, e.gu, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   const ExpertRows rows{saved->offsets + p->num_physical, cap, p->T,
                         p->has_shared, p->I};
-  h = launch_swiglu_save(rows, e.gu, e.h, saved->gu_codes, saved->gu_scales, s);
+  h = launch_swiglu_save(rows, e.gu, e.h, saved->gu_codes, saved->gu_scales,
+                         (const bf16_t*)x, p->H, saved->x_codes,
+                         saved->x_scales, s);
   if (h != hipSuccess) return MOE_ERR_HIP;
   h = launch_gemm_down(g, e.h, e.y, e.y_shared, s);
   if (h != hipSuccess) return MOE_ERR_HIP;

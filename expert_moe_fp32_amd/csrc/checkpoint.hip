@@ -231,16 +231,43 @@ __device__ __forceinline__ int intermediate_row(const ExpertRows& r, int i) {
   return r.has_shared && i < r.T ? r.cap + i : -1;
 }
 
+// A group's 128 columns on 16 lanes: this lane's codes, and the scale.
+__device__ __forceinline__ u32x2v_t checkpoint_eight(const float* v, float* scale) {
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_size(v[j]));
+  const int e = checkpoint_exponent(row16_max(top));
+  const float inv = power_of_two(-e), limit = checkpoint_limit(e);
+  *scale = power_of_two(e);
+  return u32x2v_t{checkpoint_codes(v[0], v[1], v[2], v[3], inv, limit),
+                  checkpoint_codes(v[4], v[5], v[6], v[7], inv, limit)};
+}
+
 // A wavefront's 64 lanes are 16 lanes for each of four groups of 128
-// channels, eight a lane.
+// channels, eight a lane.  Behind the rows' groups come those of the layer's
+// input (one launch of 55 us at 4096 tokens of 7168 x 2048, 32 of 256 experts
+// and the shared one, 5.2 TB/s; two launches 62, and 7.5 against 4.3 at 509
+// tokens of 1024 x 512).
 __global__ __launch_bounds__(256) void k_swiglu_save(
     ExpertRows r, const float* __restrict__ gu, bf16_t* __restrict__ h,
-    uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    uint8_t* __restrict__ codes, float* __restrict__ scales,
+    const bf16_t* __restrict__ x, int H, uint8_t* __restrict__ x_codes,
+    float* __restrict__ x_scales) {
   const int I = r.I, blocks = I / 128;
   const long count = (long)(*r.n_routed + (r.has_shared ? r.T : 0)) * blocks;
+  const long all = count + (long)r.T * (H / 128);
   const int lane = threadIdx.x & 15;
-  for (long q = (long)blockIdx.x * 16 + (threadIdx.x >> 4); q < count;
+  for (long q = (long)blockIdx.x * 16 + (threadIdx.x >> 4); q < all;
        q += (long)gridDim.x * 16) {
+    if (q >= count) {
+      const long g = q - count, at = g * 128 + lane * 8;
+      float v[8];
+      piece_values<bf16_t, 8>(*(const u32x4_t*)(x + at), v);
+      float s;
+      *(u32x2v_t*)(x_codes + at) = checkpoint_eight(v, &s);
+      if (lane == 0) x_scales[g] = s;
+      continue;
+    }
     const int i = (int)(q / blocks), n = (int)(q - (long)i * blocks);
     const long row = intermediate_row(r, i);
     const long at = row * 2 * I + n * 128 + lane * 8;
@@ -257,16 +284,9 @@ __global__ __launch_bounds__(256) void k_swiglu_save(
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      float top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_size(v[p][j]));
-      const int e = checkpoint_exponent(row16_max(top));
-      const float inv = power_of_two(-e), limit = checkpoint_limit(e);
-      u32x2v_t c;
-      c[0] = checkpoint_codes(v[p][0], v[p][1], v[p][2], v[p][3], inv, limit);
-      c[1] = checkpoint_codes(v[p][4], v[p][5], v[p][6], v[p][7], inv, limit);
-      *(u32x2v_t*)(codes + at + p * I) = c;
-      if (lane == 0) scales[row * 2 * blocks + p * blocks + n] = power_of_two(e);
+      float s;
+      *(u32x2v_t*)(codes + at + p * I) = checkpoint_eight(v[p], &s);
+      if (lane == 0) scales[row * 2 * blocks + p * blocks + n] = s;
     }
     u32x4_t o;
 #pragma unroll
@@ -415,11 +435,14 @@ hipError_t launch_restore_rows(const uint8_t* codes, const float* scales,
 }
 
 hipError_t launch_swiglu_save(const ExpertRows& r, const float* gu, bf16_t* h,
-                              uint8_t* codes, float* scales, hipStream_t s) {
-  const long most = ((long)r.cap + (r.has_shared ? r.T : 0)) * (r.I / 128);
+                              uint8_t* codes, float* scales, const bf16_t* x,
+                              int H, uint8_t* x_codes, float* x_scales,
+                              hipStream_t s) {
+  const long most = ((long)r.cap + (r.has_shared ? r.T : 0)) * (r.I / 128) +
+                    (long)r.T * (H / 128);
   const long grid = (most + 15) / 16;
   k_swiglu_save<<<(unsigned)(grid < 4096 ? grid : 4096), 256, 0, s>>>(
-      r, gu, h, codes, scales);
+      r, gu, h, codes, scales, x, H, x_codes, x_scales);
   return hipGetLastError();
 }
 

@@ -29,9 +29,11 @@ struct ExpertRows {
   int cap, T, has_shared, I;
 };
 // gu [rows][2 I] float32 (gate, then up) -> h = silu(gate) * up in bf16, and
-// the checkpoint of gu
+// the checkpoints of gu and of the layer's input x [T][H]
 hipError_t launch_swiglu_save(const ExpertRows& r, const float* gu, bf16_t* h,
-                              uint8_t* codes, float* scales, hipStream_t s);
+                              uint8_t* codes, float* scales, const bf16_t* x,
+                              int H, uint8_t* x_codes, float* x_scales,
+                              hipStream_t s);
 // Backward of it from the checkpoint: dh [rows][I] float32 (of the unweighted
 // output) -> dgu [rows][2 I] and the weighted h [rows][I] in bf16, and (unless
 // null) d_topk_w [T][k]: sum_i dh h of a pair's row, 0 for one that is not
