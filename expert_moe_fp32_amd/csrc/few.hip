@@ -86,7 +86,7 @@ __device__ __forceinline__ void few_list(const FewArgs& a, Lds& s) {
   int p = e;
   if (e >= 0 && a.l2p) {
     const int n = __popc(s.tokens[e] & ((1u << t) - 1u));
-    p = a.l2p[e * a.max_rep + n % a.rep[e]];
+    p = a.l2p[e * a.max_rep + n % min(max(a.rep[e], 1), a.max_rep)];
     if (p >= a.P) p = -1;
   }
   if (p >= 0) atomicOr(&s.phys[p], 1u << t);

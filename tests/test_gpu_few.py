@@ -158,6 +158,27 @@ def test_a_share_in_the_middle_and_replicas():
                  oracle_out(wl, ids, w, d.pair_row >= 0), "bf16", BAR)
 
 
+def test_counts_of_replicas_out_of_range():
+    """Taken as the nearest count that the map has room for, as dispatch
+    takes them."""
+    import torch
+    from expert_moe_fp32_amd.runner import to_dev
+    wl = make_workload("prefill", seed=113, T=16, H=256, I=128, E=8,
+                       num_local=8, k=4)
+    l2p = np.array([[0, 8]] + [[i, -1] for i in range(1, 7)] + [[7, 9]],
+                   dtype=np.int32)
+    rep = np.array([7, 0, 1, -3, 1, 1, 1, 2 ** 30], dtype=np.int32)
+    real = np.array([2, 1, 1, 1, 1, 1, 1, 2], dtype=np.int32)
+    dl = device_layer(wl, l2p=l2p, rep=rep, P=10,
+                      phys_to_logical=phys_to_logical_from_map(l2p, real, 10))
+    out = new_out(wl)
+    dl.forward_few(to_dev(wl.logits), None, to_dev(wl.x), out)
+    torch.cuda.synchronize()
+    ids, w, _ = omoe.route_topk(wl.logits, wl.k)
+    check_output(out[:wl.T].double().cpu().numpy(), oracle_out(wl, ids, w),
+                 "bf16", BAR)
+
+
 def test_tokens_without_a_local_expert_get_zeros():
     import torch
     from expert_moe_fp32_amd.runner import to_dev
