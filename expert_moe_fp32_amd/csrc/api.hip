@@ -922,8 +922,12 @@ namespace {
 moe_status check_experts(const moe_problem* p) {
   const moe_status st = moe_check_problem(p);
   if (st != MOE_OK) return st;
-  return p->act_dtype != MOE_BF16 || p->weight_dtype != MOE_BF16
-             ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  if (p->act_dtype != MOE_BF16 || p->weight_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  // places of a weight gradient's tiles are divided by multiplication, and
+  // rows with the shared expert's are counted, in 32 bits
+  if (p->H > 65536 || p->I > 65536 || (double)p->T * (p->k + 1) >= 2147483647.0)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 
 bool saved_ok(const moe_saved* v) {
@@ -1075,6 +1079,7 @@ moe_status moe_experts_backward(const moe_problem* p, const moe_saved* saved,
   }
   if (!d_out || !saved_ok(saved) || !al16(d_out) || !al16(d_x)) return MOE_ERR_INVALID_ARGUMENT;
   if (!workspace || ws_bytes < experts_need(p, true)) return MOE_ERR_WORKSPACE;
+  if (d_x == d_out) return MOE_ERR_INVALID_ARGUMENT;   // (read after d_x is written)
   Carver c(workspace);
   const ExpertsScratch e = carve_experts(c, p, true);
   const int cap = (int)cap_rows(p), P = p->num_physical;

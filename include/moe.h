@@ -529,7 +529,8 @@ MOE_API moe_status moe_restore_rows(const moe_rows* r, const uint8_t* codes,
 
 /* ------------------------------------------------ training the experts
  * Everything of the layer past its router -- dispatch, experts, combine -- for
- * a training step, BF16 recipe (others are UNSUPPORTED), and its gradients.
+ * a training step, BF16 recipe (others are UNSUPPORTED, and so are H or I
+ * above 65536), and its gradients.
  * The forward pass leaves what the backward needs: the permutation, and 8-bit
  * checkpoints of the layer's input and of the experts' gate and up products.
  * Intermediate rows: routed row r (r < offsets[P]) in row r, the shared
@@ -550,7 +551,8 @@ MOE_API moe_status moe_experts_workspace_size(const moe_problem* p,
                                               size_t* bytes);
 
 /*   x        [T][H] bf16
- *   topk_ids, topk_w  from moe_route_topk or moe_route_scored
+ *   topk_ids, topk_w  from moe_route_topk or moe_route_scored (a token's ids
+ *            differ)
  *   saved    every array written (rows behind the last one untouched)
  *   out      [T][H] out_dtype, as moe_layer_forward's: with unrounded gate and
  *            up products, not the checkpoint's
@@ -588,7 +590,7 @@ typedef struct {
  *   saved    as moe_experts_forward left it
  *   d_out    [T][H] bf16
  *   w        the forward's prepared weights
- *   d_x      [T][H] bf16 out, or NULL
+ *   d_x      [T][H] bf16 out, apart from d_out, or NULL
  *   d_topk_w [T][k] float32 out, or NULL
  *   grads    out, or NULL
  * At least one output is given.  T = 0 clears the weights' gradients. */

@@ -132,6 +132,20 @@ def test_training_validation(kw, status):
         m.moe_experts_workspace_size(p)
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(H=65536), WS), (dict(H=65536 + 128), UNSUP),
+    (dict(I=65536), WS), (dict(I=65536 + 128), UNSUP),
+    (dict(T=2 ** 30 - 1, k=1), WS), (dict(T=2 ** 30, k=1), UNSUP),
+], ids=str)
+def test_training_limits(kw, status):
+    p = problem(**kw)
+    assert forward(p, n=4096) == status and backward(p, n=4096) == status
+
+
+def test_d_x_is_not_d_out():
+    assert backward(problem(), d_x=P, d_out=P) == BAD
+
+
 def test_forward_arguments():
     p = problem()
     for kw in (dict(x=None), dict(ids=None), dict(w=None), dict(out=None),
