@@ -121,3 +121,28 @@ def test_scales_of_any_value_are_rounded_once():
             scales.double().repeat_interleave(128, 1)[:, :300]
         # one product in float32, then the rounding to the type
         assert ((y.double() - v).abs() <= (half + 2.0 ** -24) * v.abs()).all()
+
+
+@pytest.mark.parametrize("C", [65664, 65601])
+def test_rows_beyond_32_bits(C):
+    """2^32 elements and more: the rows at the end as in a small call."""
+    import torch
+    import expert_moe_fp32_amd as m
+    T, n = 65536, -(-C // 128)
+    assert T * C > 2 ** 32
+    x = torch.zeros(T, C, dtype=torch.bfloat16, device="cuda")
+    last = rows_of(5, C, "bf16", 0, 11)
+    x[-5:] = last
+    codes = torch.full((T, C), 77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((T, n), 7.0, device="cuda")
+    small = torch.empty(5, C, dtype=torch.uint8, device="cuda"), torch.empty(5, n, device="cuda")
+    m.moe_checkpoint_rows(m.make_rows(T, C, dtype="bf16"), x, codes, scales)
+    m.moe_checkpoint_rows(m.make_rows(5, C, dtype="bf16"), last, *small)
+    torch.cuda.synchronize()
+    assert torch.equal(codes[-5:], small[0]) and torch.equal(scales[-5:], small[1])
+    assert not codes[:-5:64].any() and (scales[:-5] == 1.0).all()
+    x.fill_(9.0)
+    m.moe_restore_rows(m.make_rows(T, C, dtype="bf16"), codes, scales, x)
+    m.moe_restore_rows(m.make_rows(5, C, dtype="bf16"), *small, last)
+    torch.cuda.synchronize()
+    assert torch.equal(x[-5:], last) and not x[:-5:64].any()

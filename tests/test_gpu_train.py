@@ -410,6 +410,45 @@ def test_replays_from_a_graph():
         assert torch.equal(v, eager[n]), n
 
 
+def test_intermediate_arrays_beyond_32_bits():
+    """More than 2^32 elements of gate and up: 70 copies of 1000 tokens get
+    what the first copy gets, bit for bit (a row's result does not depend on
+    its place), and the first what a pass of 1000 gets, to two roundings.  The
+    weights' gradients are 70 times the pass's: a sum of n products in float32
+    is within n u of the sum of their magnitudes, about 20 times such a sum of
+    random signs here (1000 independent terms, 70 times over: 0.8 sqrt(1000))."""
+    import torch
+    copies, kw = 70, dict(H=128, I=16384, E=2, num_local=2, k=2, shared=False)
+    wl = make_workload("prefill", seed=212, T=1000, **kw)
+    one = Step(wl)
+    one.forward()
+    one.backward()
+    torch.cuda.synchronize()
+
+    class Copies(type(wl)):
+        logits = property(lambda self: np.tile(wl.logits, (copies, 1)))
+        x = property(lambda self: np.tile(wl.x, (copies, 1)))
+
+    big = make_workload("prefill", seed=212, T=1000 * copies, **kw)
+    big.__class__ = Copies
+    s = Step(big)
+    s.d_out = one.d_out.repeat(copies, 1)
+    assert s.cap * 2 * wl.I > 2 ** 32
+    s.forward()
+    s.backward()
+    torch.cuda.synchronize()
+    for name in ("out", "d_x", "d_w"):
+        v = getattr(s.b, name).view(copies, 1000, -1)
+        assert torch.equal(v, v[:1].expand_as(v)), name
+        a, b = v[0].double(), getattr(one.b, name).double().view(1000, -1)
+        assert (a - b).norm() <= 2 * B * b.norm(), name
+    n = big.T * 2
+    for name, v in s.b.grads.items():
+        if v.numel():
+            ref = copies * one.b.grads[name].double()
+            assert (v.double() - ref).norm() <= 20 * n * U * ref.norm(), name
+
+
 def test_two_streams_at_once():
     import torch
     runs = [(Step(make_workload("prefill", seed=210 + i, T=T, H=256, I=256,
