@@ -15,6 +15,10 @@ Modules:
 * ``fp8``   OCP E4M3 decode/encode and the block / per-token quantisers;
 * ``eplb``  redundant-expert map for skewed routing and the load-balancing
             placement policy with its load simulation;
+* ``block`` scored routing, the residual norm, combine and norm, and their
+            gradients;
+* ``train`` 8-bit checkpoints of rows, and the experts' forward and backward
+            pass around them;
 * ``arith`` the pages' byte and parameter arithmetic.
 
 Parity pins live in ``tests/test_oracle_*.py``.  Parity unpinned: the exact bits
