@@ -891,7 +891,9 @@ moe_status moe_check_rows(const moe_rows* r) {
     return MOE_ERR_INVALID_ARGUMENT;
   if (r->dtype < MOE_F32 || r->dtype > MOE_FP8_E4M3) return MOE_ERR_INVALID_ARGUMENT;
   if (r->dtype == MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
-  // groups of 128 columns are counted in 32 bits
+  // a row's columns up to the end of its last group, and the groups of all
+  // rows, are counted in 32 bits
+  if (r->cols > 2147483647 - 127) return MOE_ERR_UNSUPPORTED;
   if ((double)r->rows * (((double)r->cols + 127.0) / 128.0) >= 2147483647.0)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

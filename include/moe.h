@@ -509,7 +509,8 @@ typedef struct {
   int64_t stride;  /* elements between rows, at least cols                    */
 } moe_rows;
 
-/* Validate a description of rows (host only). */
+/* Validate a description of rows (host only).  UNSUPPORTED: more than 2^31 -
+ * 128 columns, or 2^31 - 1 groups or more in all rows. */
 MOE_API moe_status moe_check_rows(const moe_rows* r);
 
 /*   src    [rows][stride], the first cols of each row read

@@ -82,6 +82,18 @@ def test_rows_validation(kw, status):
         assert m.moe_restore_rows(r, P, P, P, stream=0, check=False) == status
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols,status", [
+    (2 ** 31 - 129, L.MOE_OK), (2 ** 31 - 128, L.MOE_OK),
+    (2 ** 31 - 127, UNSUP), (2 ** 31 - 1, UNSUP)])
+def test_columns_whose_last_group_leaves_32_bits(cols, status, dtype):
+    r = m.make_rows(1, cols, dtype=dtype)
+    assert m.moe_check_rows(r) == status
+    if status != L.MOE_OK:
+        assert m.moe_checkpoint_rows(r, P, P, P, stream=0, check=False) == status
+        assert m.moe_restore_rows(r, P, P, P, stream=0, check=False) == status
+
+
 def test_rows_arguments():
     r = m.make_rows(4, 100)
     r.dtype = 7

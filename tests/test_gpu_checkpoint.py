@@ -146,3 +146,32 @@ def test_rows_beyond_32_bits(C):
     m.moe_restore_rows(m.make_rows(5, C, dtype="bf16"), *small, last)
     torch.cuda.synchronize()
     assert torch.equal(x[-5:], last) and not x[:-5:64].any()
+
+
+@pytest.mark.parametrize("cut", [0, 61])
+def test_the_longest_row(cut):
+    """One row of almost 2^31 columns is what its groups are as rows of their
+    own (and the cut group at its end)."""
+    import torch
+    import expert_moe_fp32_amd as m
+    C = 2 ** 31 - 128 - cut
+    n, whole = -(-C // 128), C // 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(C, device="cuda", dtype=torch.bfloat16, generator=g)
+    codes, parts = (torch.full((C,), 77, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales, own = (torch.full((n,), 7.0, device="cuda") for _ in range(2))
+    m.moe_checkpoint_rows(m.make_rows(1, C), x, codes, scales)
+    m.moe_checkpoint_rows(m.make_rows(whole, 128), x, parts, own)
+    if cut:
+        m.moe_checkpoint_rows(m.make_rows(1, C % 128), x[whole * 128:],
+                              parts[whole * 128:], own[whole:])
+    torch.cuda.synchronize()
+    assert torch.equal(codes, parts) and torch.equal(scales, own)
+    y = torch.full((C,), 9.0, dtype=torch.bfloat16, device="cuda")
+    m.moe_restore_rows(m.make_rows(1, C), codes, scales, y)
+    m.moe_restore_rows(m.make_rows(whole, 128), codes, scales, x)
+    if cut:
+        m.moe_restore_rows(m.make_rows(1, C % 128), codes[whole * 128:],
+                           scales[whole:], x[whole * 128:])
+    torch.cuda.synchronize()
+    assert torch.equal(y, x)
