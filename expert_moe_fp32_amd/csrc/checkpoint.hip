@@ -7,6 +7,8 @@
 // columns, whose largest magnitude is four DPP steps and at most one exchange
 // between rows.  8192 x 7168 bf16: 32 us to codes, 30 us back (5.6 and 5.9
 // TB/s; a copy of 256 MiB 5.3); 1021 x 2501 float32, rows at any alignment: 4.6.
+#include <algorithm>
+
 #include "checkpoint.h"
 #include "rows.h"
 #include "train.h"
@@ -54,11 +56,12 @@ constexpr int kRowThreads = 256;
 
 // A workgroup takes U runs of kRowThreads pieces of W columns; the pieces of
 // a row are padded to whole groups.  FIT: kAligned (C a multiple of W, rows
-// and codes aligned to their pieces) or kAny.
+// and codes aligned to their pieces) or kAny.  `first`: the launch's first group.
 template <typename T, Fit FIT, int U>
 __global__ __launch_bounds__(kRowThreads) void k_checkpoint_rows(
-    const T* __restrict__ src, long stride, uint32_t groups, uint32_t per_row,
-    int C, uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    const T* __restrict__ src, long stride, uint32_t first, uint32_t groups,
+    uint32_t per_row, int C, uint8_t* __restrict__ codes,
+    float* __restrict__ scales) {
   constexpr int W = 16 / (int)sizeof(T), LANES = 128 / W;
   constexpr uint32_t kPer = kRowThreads / LANES;       // groups a run
   const int lane = threadIdx.x & (LANES - 1);
@@ -68,7 +71,7 @@ __global__ __launch_bounds__(kRowThreads) void k_checkpoint_rows(
   Raw<T, W> r[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    g[u] = (blockIdx.x * U + u) * kPer + threadIdx.x / LANES;
+    g[u] = first + (blockIdx.x * U + u) * kPer + threadIdx.x / LANES;
     const uint32_t gg = min(g[u], groups - 1);
     t[u] = gg / per_row;
     const int n = (int)(gg - (uint32_t)t[u] * per_row);
@@ -110,8 +113,8 @@ __global__ __launch_bounds__(kRowThreads) void k_checkpoint_rows(
 template <typename T, Fit FIT, int U>
 __global__ __launch_bounds__(kRowThreads) void k_restore_rows(
     const uint8_t* __restrict__ codes, const float* __restrict__ scales,
-    uint32_t groups, uint32_t per_row, int C, T* __restrict__ dst,
-    long stride) {
+    uint32_t first, uint32_t groups, uint32_t per_row, int C,
+    T* __restrict__ dst, long stride) {
   constexpr int W = 16 / (int)sizeof(T), LANES = 128 / W;
   constexpr uint32_t kPer = kRowThreads / LANES;
   typedef typename CodesOf<W>::V Codes;
@@ -122,7 +125,7 @@ __global__ __launch_bounds__(kRowThreads) void k_restore_rows(
   float s[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t g = (blockIdx.x * U + u) * kPer + threadIdx.x / LANES;
+    const uint32_t g = first + (blockIdx.x * U + u) * kPer + threadIdx.x / LANES;
     const uint32_t gg = min(g, groups - 1);
     t[u] = gg / per_row;
     const int n = (int)(gg - (uint32_t)t[u] * per_row);
@@ -176,6 +179,22 @@ __global__ __launch_bounds__(kRowThreads) void k_restore_rows(
 // spread over the CUs.
 constexpr uint32_t kManyRuns = 8192;
 
+// A launch has less than 2^32 threads (a larger grid runs only in part), so
+// more groups than this take several.
+constexpr uint32_t kLaunchBlocks = 1u << 23;
+
+// `run`(first group, workgroups) over all groups, `per` of them a workgroup
+template <class F>
+hipError_t launch_groups(uint32_t groups, uint32_t per, F run) {
+  const uint32_t blocks = (groups + per - 1) / per;
+  for (uint32_t b = 0; b < blocks; b += kLaunchBlocks) {
+    run(b * per, std::min(blocks - b, kLaunchBlocks));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <typename T>
 hipError_t checkpoint_rows(const T* src, long Tn, int C, long stride,
                            uint8_t* codes, float* scales, hipStream_t s) {
@@ -186,17 +205,17 @@ hipError_t checkpoint_rows(const T* src, long Tn, int C, long stride,
   const bool fits = C % W == 0 && stride % W == 0 &&
                     ((uintptr_t)src & 15) == 0 && ((uintptr_t)codes & (W - 1)) == 0;
 #define RUN(FIT, U)                                                           \
-  k_checkpoint_rows<T, FIT, U><<<(runs + U - 1) / U, kRowThreads, 0, s>>>(    \
-      src, stride, groups, per_row, C, codes, scales)
+  return launch_groups(groups, per * U, [&](uint32_t first, uint32_t blocks) { \
+    k_checkpoint_rows<T, FIT, U><<<blocks, kRowThreads, 0, s>>>(              \
+        src, stride, first, groups, per_row, C, codes, scales);               \
+  })
   if (runs >= kManyRuns) {
     if (fits) RUN(kAligned, 4);
-    else RUN(kAny, 4);
-  } else {
-    if (fits) RUN(kAligned, 1);
-    else RUN(kAny, 1);
+    RUN(kAny, 4);
   }
+  if (fits) RUN(kAligned, 1);
+  RUN(kAny, 1);
 #undef RUN
-  return hipGetLastError();
 }
 
 template <typename T>
@@ -209,17 +228,17 @@ hipError_t restore_rows(const uint8_t* codes, const float* scales, long Tn,
   const bool fits = C % W == 0 && stride % W == 0 &&
                     ((uintptr_t)dst & 15) == 0 && ((uintptr_t)codes & (W - 1)) == 0;
 #define RUN(FIT, U)                                                           \
-  k_restore_rows<T, FIT, U><<<(runs + U - 1) / U, kRowThreads, 0, s>>>(       \
-      codes, scales, groups, per_row, C, dst, stride)
+  return launch_groups(groups, per * U, [&](uint32_t first, uint32_t blocks) { \
+    k_restore_rows<T, FIT, U><<<blocks, kRowThreads, 0, s>>>(                 \
+        codes, scales, first, groups, per_row, C, dst, stride);               \
+  })
   if (runs >= kManyRuns) {
     if (fits) RUN(kAligned, 4);
-    else RUN(kAny, 4);
-  } else {
-    if (fits) RUN(kAligned, 1);
-    else RUN(kAny, 1);
+    RUN(kAny, 4);
   }
+  if (fits) RUN(kAligned, 1);
+  RUN(kAny, 1);
 #undef RUN
-  return hipGetLastError();
 }
 
 // ------------------------------------------- the experts' activation

@@ -175,3 +175,40 @@ def test_the_longest_row(cut):
                            scales[whole:], x[whole * 128:])
     torch.cuda.synchronize()
     assert torch.equal(y, x)
+
+
+@pytest.mark.parametrize("T,dtype", [(2 ** 29 + 4099, "f32"),
+                                     (2 ** 30 + 4099, "bf16")])
+def test_more_groups_than_a_launch_has_threads_for(T, dtype):
+    """Rows of one column, more than 2^29 (float32) or 2^30:
+    every one as the same value in a small call."""
+    import torch
+    import expert_moe_fp32_amd as m
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    n = 4096
+    g = torch.Generator(device="cuda").manual_seed(6)
+    part = torch.randn(n, device="cuda", generator=g).mul_(3).exp().to(dt)
+    codes, scales = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(n, device="cuda")
+    back = torch.empty(n, dtype=dt, device="cuda")
+    few = m.make_rows(n, 1, dtype=dtype)
+    m.moe_checkpoint_rows(few, part, codes, scales)
+    m.moe_restore_rows(few, codes, scales, back)
+    x = torch.empty(T, dtype=dt, device="cuda")
+    all_codes = torch.full((T + 1,), 77, dtype=torch.uint8, device="cuda")
+    all_scales = torch.full((T + 1,), 7.0, device="cuda")
+    whole = T // n * n
+
+    def copies(a, of):
+        return (torch.equal(a[:whole].view(-1, n), of.expand(whole // n, n)) and
+                torch.equal(a[whole:T], of[:T - whole]))
+    x[:whole].view(-1, n).copy_(part.expand(whole // n, n))
+    x[whole:] = part[:T - whole]
+    many = m.make_rows(T, 1, dtype=dtype)
+    m.moe_checkpoint_rows(many, x, all_codes, all_scales)
+    torch.cuda.synchronize()
+    assert copies(all_codes, codes) and copies(all_scales, scales)
+    assert all_codes[T] == 77 and all_scales[T] == 7.0
+    y = torch.full((T + 1,), 9.0, dtype=dt, device="cuda")
+    m.moe_restore_rows(many, all_codes, all_scales, y)
+    torch.cuda.synchronize()
+    assert copies(y, back) and y[T] == 9.0
