@@ -113,10 +113,25 @@ __global__ __launch_bounds__(256) void k_combine(
   }
 }
 
+// A launch has less than 2^32 threads (a larger grid runs only in part), so
+// more tokens than this take several.
+static constexpr int kCombineTokens = 1 << 23;
+
 hipError_t launch_combine(const float* y_perm, const int32_t* pair_row,
                           const float* w, const float* y_shared, int T, int H,
                           int k, int out_dtype, void* out, hipStream_t s) {
   if (T == 0) return hipSuccess;
+  if (T > kCombineTokens) {
+    for (long t = 0; t < T; t += kCombineTokens) {
+      const size_t row = (size_t)t * H, pair = (size_t)t * k;
+      const hipError_t e = launch_combine(
+          y_perm, pair_row + pair, w ? w + pair : nullptr,
+          y_shared ? y_shared + row : nullptr, (int)min(T - t, (long)kCombineTokens), H, k,
+          out_dtype, (char*)out + row * (out_dtype == MOE_BF16 ? 2 : 4), s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   // column slices (multiples of 256 groups of 4) so that small batches
   // still launch about 2048 workgroups
   const int H4 = H / 4;

@@ -164,3 +164,31 @@ def test_fp8_quantiser_every_bf16_value():
     got = run_dispatch(wl)
     check_against_oracle(wl, got)
     assert np.all(got["x_scales"] == 1.0)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_combine_of_more_tokens_than_a_launch_has_workgroups_for(out):
+    """2^24 + 4099 tokens, 4096 of them over and over: each as in a call of
+    4096."""
+    import torch
+    import expert_moe_fp32_amd as m
+    n, T, H, k = 4096, 2 ** 24 + 4099, 128, 2
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(18)
+    y = torch.randn(500, H, device="cuda", generator=g)
+    rows = torch.randint(-1, 500, (n, k), device="cuda", generator=g, dtype=torch.int32)
+    w = torch.rand(n, k, device="cuda", generator=g)
+    ys = torch.randn(n, H, device="cuda", generator=g)
+    many = lambda t: t.repeat(-(-T // n), 1)[:T].contiguous()
+
+    def run(T, rows, w, ys):
+        o = torch.full((T + 1, H), 7.0, dtype=dt, device="cuda")
+        m.moe_combine(m.make_problem(T, H, 128, 2, k, has_shared=True, out=out),
+                      y, rows, w, ys, o)
+        torch.cuda.synchronize()
+        assert (o[T] == 7.0).all()
+        return o[:T]
+    ref, v = run(n, rows, w, ys), run(T, many(rows), many(w), many(ys))
+    whole = T // n * n
+    assert torch.equal(v[:whole].view(-1, n, H), ref.expand(whole // n, n, H))
+    assert torch.equal(v[whole:], ref[:T - whole])

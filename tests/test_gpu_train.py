@@ -532,3 +532,49 @@ def test_a_training_step():
         err = (got.double().cpu() - ref).pow(2).mean().sqrt() / ref.pow(2).mean().sqrt()
         print(name, float(err), flush=True)
         assert err <= 0.125, (name, float(err))
+
+
+def copies_of(v, n):
+    """Whether v's rows are its first n over and over."""
+    import torch
+    whole = v.shape[0] // n
+    a = v[:whole * n].view(whole, n, -1)
+    return (torch.equal(a, a[:1].expand_as(a)) and
+            torch.equal(v[whole * n:], v[:v.shape[0] - whole * n]))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_more_tokens_than_a_launch_has_workgroups_for(shared):
+    """2^24 + 4099 tokens of one expert, 4096 of them over and over: every
+    copy gets what the first gets, bit for bit, and the first what a pass of
+    4096 gets, to two roundings."""
+    import torch
+    import expert_moe_fp32_amd as m
+    from expert_moe_fp32_amd.runner import DeviceLayer
+    n, H, I = 4096, 128, 128
+    g = torch.Generator().manual_seed(17)
+    bits = lambda t: t.bfloat16().view(torch.int16).numpy().view(np.uint16)
+    expert = lambda: dict(wg=bits(torch.randn(H, I, generator=g) / 11),
+                          wu=bits(torch.randn(H, I, generator=g) / 11),
+                          wd=bits(torch.randn(I, H, generator=g) / 11))
+    first, also = expert(), expert()
+    x, d_out = (torch.randn(n, H, generator=g).bfloat16().cuda() for _ in range(2))
+    w = torch.rand(n, 1, generator=g).cuda()
+
+    def run(T):
+        dl = DeviceLayer(m.make_problem(T, H, I, 1, 1, has_shared=shared),
+                         [first], also if shared else None)
+        many = lambda t: t.repeat(-(-T // n), 1)[:T].contiguous()
+        ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+        b = dl.train_buffers()
+        for t in (b.out, b.d_x, b.d_w):
+            t.fill_(7.0)
+        dl.experts_forward(b, many(x), ids, many(w))
+        dl.experts_backward(b, many(d_out))
+        torch.cuda.synchronize()
+        return b
+    small, big = run(n), run(2 ** 24 + 4099)
+    for name in ("out", "d_x", "d_w"):
+        v, ref = getattr(big, name), getattr(small, name).double()
+        assert copies_of(v, n), name
+        assert (v[:n].double() - ref).norm() <= 2 * B * ref.norm(), name
