@@ -9,6 +9,8 @@
 // loads before it accumulates, in float32 and slot order, with one rounding
 // to the output type.  Without route weights every row counts once (the sum
 // of the rows' gradients over a token).
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -126,7 +128,7 @@ hipError_t launch_combine(const float* y_perm, const int32_t* pair_row,
       const size_t row = (size_t)t * H, pair = (size_t)t * k;
       const hipError_t e = launch_combine(
           y_perm, pair_row + pair, w ? w + pair : nullptr,
-          y_shared ? y_shared + row : nullptr, (int)min(T - t, (long)kCombineTokens), H, k,
+          y_shared ? y_shared + row : nullptr, (int)std::min(T - t, (long)kCombineTokens), H, k,
           out_dtype, (char*)out + row * (out_dtype == MOE_BF16 ? 2 : 4), s);
       if (e != hipSuccess) return e;
     }

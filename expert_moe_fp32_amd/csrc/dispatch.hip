@@ -16,6 +16,8 @@
 //      (offsets).
 //   3. k_permute: the ballots again give each pair its rank inside the
 //      wavefront; block base + earlier wavefronts + that rank is n.
+#include <algorithm>
+
 #include "route_row.h"
 
 namespace moe {
@@ -596,10 +598,16 @@ hipError_t launch_quant_rows_fp8(const bf16_t* x, int T, int H,
                                  uint8_t* codes, float* scales,
                                  hipStream_t s) {
   const long n8 = (long)T * H / 8;         // H % 128 == 0
-  if (n8 == 0) return hipSuccess;
-  k_quant_rows_fp8<<<(unsigned)((n8 + 255) / 256), 256, 0, s>>>(x, n8, codes,
-                                                               scales);
-  return hipGetLastError();
+  // less than 2^32 threads a launch (a larger grid runs only in part)
+  constexpr long kChunks = 1l << 31;
+  for (long i = 0; i < n8; i += kChunks) {
+    const long n = std::min(n8 - i, kChunks);
+    k_quant_rows_fp8<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
+        x + 8 * i, n, codes + 8 * i, scales + i / 16);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 __global__ void k_fill_i32(int32_t* p, int32_t v, size_t n) {

@@ -9,6 +9,8 @@
 // single-workgroup histogram of the chosen ids with one LDS copy per
 // wavefront; it stores the counts, so no atomics reach global memory (on
 // skewed routing the hot experts' counters would serialise them).
+#include <algorithm>
+
 #include "block.h"
 #include "route_row.h"
 
@@ -116,9 +118,22 @@ hipError_t launch_count_ids(const int32_t* ids, int n, int E, int32_t* counts,
   return hipGetLastError();
 }
 
+// A launch has less than 2^32 threads (a larger grid runs only in part), so
+// more tokens than this take several.
+static constexpr int kRouteTokens = 1 << 25;
+
 hipError_t launch_route_topk(const float* logits, const float* bias, int T,
                              int E, int k, int32_t* ids, float* w,
                              int32_t* counts, hipStream_t s) {
+  if (T > kRouteTokens) {
+    for (long t = 0; t < T; t += kRouteTokens) {
+      const hipError_t e = launch_route_topk(
+          logits + t * E, bias, (int)std::min(T - t, (long)kRouteTokens), E, k,
+          ids + t * k, w + t * k, nullptr, s);
+      if (e != hipSuccess) return e;
+    }
+    return counts ? launch_count_ids(ids, T * k, E, counts, s) : hipSuccess;
+  }
   if (E <= 256) {
     dim3 grid((T + 15) / 16), block(256);
 #define ROUTE_ROWS(KPL)                                                        \

@@ -192,3 +192,36 @@ def test_combine_of_more_tokens_than_a_launch_has_workgroups_for(out):
     whole = T // n * n
     assert torch.equal(v[:whole].view(-1, n, H), ref.expand(whole // n, n, H))
     assert torch.equal(v[whole:], ref[:T - whole])
+
+
+def test_more_fp8_rows_than_a_launch_has_threads_for():
+    """2^35 elements and more to quantise, 4096 rows over and over: codes and
+    scales as in a call of 4096 rows."""
+    import torch
+    import expert_moe_fp32_amd as m
+    n, T, H = 4096, 2 ** 21 + 4099, 16384
+    g = torch.Generator(device="cuda").manual_seed(20)
+    part = torch.randn(n, H, device="cuda", generator=g).bfloat16()
+
+    def run(T, x):
+        p = m.make_problem(T, H, 128, 1, 1, wdt="fp8")
+        z = lambda *s, dt=torch.int32: torch.empty(s, dtype=dt, device="cuda")
+        ids, w = z(T, 1).zero_(), z(T, 1, dt=torch.float32).fill_(1.0)
+        codes, scales = z(T, H, dt=torch.uint8), z(T, H // 128, dt=torch.float32)
+        ws = z(m.moe_dispatch_workspace_size(p), dt=torch.uint8)
+        for t in (codes, scales, ws):
+            t.fill_(3)
+        m.moe_dispatch(p, x, ids, w, None, None, codes, scales, z(2), z(T),
+                       z(T, dt=torch.float32), z(T, 1), ws, ws.numel())
+        torch.cuda.synchronize()
+        return codes, scales
+    small = run(n, part)
+    whole = T // n * n
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    x[:whole].view(-1, n, H).copy_(part.expand(whole // n, n, H))
+    x[whole:] = part[:T - whole]
+    for v, ref in zip(run(T, x), small):
+        assert all(torch.equal(v[i:i + n], ref) for i in range(0, whole, n))
+        assert torch.equal(v[whole:], ref[:T - whole])
+    del x, v
+    torch.cuda.empty_cache()

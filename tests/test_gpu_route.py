@@ -74,3 +74,31 @@ def test_route_is_deterministic():
     a = run_route(wl)
     b = run_route(wl)
     assert all(np.array_equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("T,E", [(2 ** 28 + 4099, 2), (2 ** 26 + 4099, 257)])
+def test_more_tokens_than_a_launch_has_workgroups_for(T, E):
+    """4096 tokens over and over: each as in a call of 4096."""
+    import torch
+    import expert_moe_fp32_amd as m
+    n, k = 4096, 1
+    g = torch.Generator(device="cuda").manual_seed(19)
+    part = torch.randn(n, E, device="cuda", generator=g)
+    logits = torch.empty(T, E, device="cuda")
+    whole = T // n * n
+    logits[:whole].view(-1, n, E).copy_(part.expand(whole // n, n, E))
+    logits[whole:] = part[:T - whole]
+
+    def run(T, rows):
+        ids = torch.full((T + 1, k), 99, dtype=torch.int32, device="cuda")
+        w = torch.full((T + 1, k), 99.0, device="cuda")
+        counts = torch.empty(E, dtype=torch.int32, device="cuda")
+        m.moe_route_topk(m.make_problem(T, 128, 128, E, k), rows, None, ids, w,
+                         counts)
+        torch.cuda.synchronize()
+        assert (ids[T] == 99).all() and (w[T] == 99.0).all()
+        assert torch.equal(counts, torch.bincount(ids[:T, 0], minlength=E).int())
+        return ids[:T, 0], w[:T, 0]
+    for ref, v in zip(run(n, part), run(T, logits)):
+        assert torch.equal(v[:whole].view(-1, n), ref.expand(whole // n, n))
+        assert torch.equal(v[whole:], ref[:T - whole])
