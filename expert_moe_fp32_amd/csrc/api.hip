@@ -819,7 +819,12 @@ FewScratch carve_few(Carver& c, const moe_problem* p) {
 moe_status check_few(const moe_problem* p) {
   const moe_status st = moe_check_problem(p);
   if (st != MOE_OK) return st;
-  return p->T > MOE_FEW_TOKENS || p->act_dtype != MOE_BF16 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  if (p->T > MOE_FEW_TOKENS || p->act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  // a workgroup for 16 of H in one launch of less than 2^32 threads; 16 of I
+  // of every expert in use counted in 32 bits
+  if (p->H >= 1 << 27 || (double)few_entries(p) * (p->I / 16) >= 2147483647.0 - 512.0)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 }  // namespace
 

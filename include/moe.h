@@ -484,8 +484,10 @@ MOE_API moe_status moe_layer_forward_scored(
  *   h        rounded to bf16, as in the BF16 recipe
  *   sums     in float32; out rounded once
  * Arguments as in the two; expert_counts may be NULL.  T = 0 clears it.
- * UNSUPPORTED for T > MOE_FEW_TOKENS.  Identical inputs give identical
- * outputs. */
+ * UNSUPPORTED for T > MOE_FEW_TOKENS, for H of 2^27 and more, and where I / 16
+ * times the experts that 16 tokens can use (at most 16 k, at most
+ * num_physical, and the shared one) reaches 2^31 - 513.  Identical inputs give
+ * identical outputs. */
 #define MOE_FEW_TOKENS 16
 MOE_API moe_status moe_layer_few_workspace_size(const moe_problem* p,
                                                 size_t* bytes);

@@ -46,6 +46,22 @@ def test_few_validation(kw, status):
     assert e.value.status == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(H=2 ** 27 - 128), WS), (dict(H=2 ** 27), UNSUP),
+    # 4 experts here: I / 16 of each
+    (dict(I=2 ** 31 - 128), WS),
+    (dict(I=2 ** 31 - 128, num_local=16, T=1), UNSUP),
+    (dict(I=2 ** 30, num_local=16, E=256, k=16), WS),
+    (dict(I=2 ** 30, num_local=16, E=256, k=16, has_shared=True), WS),
+    (dict(I=2 ** 30, num_local=31, E=256, k=16, has_shared=True), UNSUP),
+    (dict(I=2 ** 27, num_local=256, E=256, k=16), UNSUP),
+    (dict(I=2 ** 27 - 128, num_local=256, E=256, k=16), WS),
+    (dict(I=2 ** 27 - 128, num_local=256, E=256, k=16, has_shared=True), UNSUP),
+], ids=str)
+def test_few_limits(kw, status):
+    assert few(problem(**kw), n=4096) == status
+
+
 def test_few_arguments():
     p = problem()
     need = m.moe_layer_few_workspace_size(p)
