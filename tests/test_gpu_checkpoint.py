@@ -212,3 +212,34 @@ def test_more_groups_than_a_launch_has_threads_for(T, dtype):
     m.moe_restore_rows(many, all_codes, all_scales, y)
     torch.cuda.synchronize()
     assert copies(y, back) and y[T] == 9.0
+
+
+@pytest.mark.parametrize("C,pad", [(2048, 0), (2001, 2), (1, 0), (130, 6)])
+def test_large_float32_calls(C, pad):
+    """From 65536 groups on a workgroup takes four runs of them: every row as
+    in calls of 64 rows."""
+    import torch
+    import expert_moe_fp32_amd as m
+    n = -(-C // 128)
+    T = 65536 // n + 77
+    assert T * n >= 65536 and 64 * n < 65536
+    x = rows_of(T, C, "f32", pad, C)
+    codes, part = (torch.full((T + 1, C), 77, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales, own = (torch.full((T + 1, n), 7.0, device="cuda") for _ in range(2))
+    y, back = (torch.full((T + 1, C + pad), 9.0, device="cuda") for _ in range(2))
+    d = m.make_rows(T, C, dtype="f32", stride=C + pad)
+    m.moe_checkpoint_rows(d, x, codes, scales)
+    m.moe_restore_rows(d, codes, scales, y)
+    for at in range(0, T, 64):
+        d = m.make_rows(min(64, T - at), C, dtype="f32", stride=C + pad)
+        m.moe_checkpoint_rows(d, x[at:], part[at:], own[at:])
+        m.moe_restore_rows(d, part[at:], own[at:], back[at:])
+    torch.cuda.synchronize()
+    assert torch.equal(codes, part) and torch.equal(scales, own)
+    assert torch.equal(y, back)
+    assert (y[:, C:] == 9.0).all() and (y[T] == 9.0).all()
+    assert (codes[T] == 77).all() and (scales[T] == 7.0).all()
+    some = np.r_[0, T // 3, T - 1]
+    rc, rs = ot.checkpoint(x[some, :C].double().cpu().numpy())
+    assert np.array_equal(codes[:T].cpu().numpy()[some], rc)
+    assert np.array_equal(scales[:T].cpu().numpy()[some], rs)

@@ -73,6 +73,32 @@ def test_against_the_oracle(name, kw, shared):
         check_output(got, ref, wl.out, BAR, f"{name} {kw}")
 
 
+@pytest.mark.parametrize("name", ["prefill", "fp8"])
+@pytest.mark.parametrize("T,H,I", [(16, 512, 640), (16, 1152, 1152),
+                                   (3, 1280, 1152), (16, 128, 1664)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_more_items_than_workgroups(name, T, H, I, shared):
+    """The first kernel's 512 workgroups take two, three or four of the items
+    (16 channels of an expert in use), not all of them equally many; H of 128
+    and 512 leave some wavefronts without a share of the reduction."""
+    import torch
+    from expert_moe_fp32_amd.runner import to_dev
+    wl = make_workload(name, seed=114, T=T, H=H, I=I, E=16, num_local=16,
+                       k=16, shared=shared)
+    items = (16 + shared) * I // 16          # every expert is in use
+    print(name, T, H, I, shared, items, flush=True)
+    assert items > (512 if I == 640 else 1024) and items % 512
+    dl, out = device_layer(wl), new_out(wl, wl.out)
+    counts = torch.full((17,), 9, dtype=torch.int32, device="cuda")
+    dl.forward_few(to_dev(wl.logits), None, to_dev(wl.x), out, counts)
+    torch.cuda.synchronize()
+    ids, w, c = omoe.route_topk(wl.logits, wl.k)
+    assert (c == T).all() and np.array_equal(counts[:16].cpu().numpy(), c)
+    assert counts[16] == 9 and (out[T] == 5.0).all()
+    check_output(out[:T].double().cpu().numpy(), oracle_out(wl, ids, w),
+                 wl.out, BAR, f"{name} {T} {H} {I}")
+
+
 @pytest.mark.parametrize("T", list(range(1, 17)))
 def test_every_count_of_tokens(T):
     """Against the general layer on the same weights (bf16 recipe: both round

@@ -250,6 +250,24 @@ def test_on_large_tiles(kw, grads):
     check_step(Step(make_workload("prefill", seed=211, **kw), grads))
 
 
+STRIPS = [
+    # outputs of 6 x 9 and 5 x 6 tiles of 256 x 256 (the last ones half), in
+    # strips of four tiles along M: 4 + 2 and 4 + 1
+    (dict(T=40, H=1408, I=1152, E=3, num_local=3, k=2, shared=True), "f32"),
+    # 9 x 11 and 6 x 9: strips of 4 + 4 + 1 and 4 + 2
+    (dict(T=23, H=2176, I=1408, E=4, num_local=2, k=2, shared=False), "bf16"),
+    # 7 x 12 and 6 x 7: strips of 4 + 3 and 4 + 2; groups of several quads
+    (dict(T=300, H=1792, I=1536, E=1, num_local=1, k=1, shared=False), "f32"),
+]
+
+
+@pytest.mark.parametrize("kw,grads", STRIPS, ids=str)
+def test_weight_gradients_of_several_strips(kw, grads):
+    print(kw, grads, flush=True)
+    assert kw["H"] > 1024 and kw["I"] > 1024
+    check_step(Step(make_workload("prefill", seed=213, **kw), grads))
+
+
 def test_a_share_in_the_middle_and_replicas():
     wl = make_workload("prefill", seed=202, T=70, H=256, I=128, E=16,
                        num_local=8, k=4, shared=True)
@@ -447,6 +465,41 @@ def test_intermediate_arrays_beyond_32_bits():
         if v.numel():
             ref = copies * one.b.grads[name].double()
             assert (v.double() - ref).norm() <= 20 * n * U * ref.norm(), name
+
+
+def test_weight_gradients_of_rows_beyond_32_bits():
+    """Gradients of only the last of 70 copies of 1000 tokens, whose rows of
+    the second expert lie past 2^32 elements of gate and up: what a pass of
+    these 1000 gives, in norm to two roundings of the products' factors (the
+    order of the float32 sums may differ: each is within (n + 1) u, n = 1000, of
+    terms whose magnitudes add up to some 25 times the result, 1.5e-3)."""
+    import torch
+    copies, kw = 70, dict(H=128, I=16384, E=2, num_local=2, k=2, shared=False)
+    wl = make_workload("prefill", seed=212, T=1000, **kw)
+    one = Step(wl)
+    one.forward()
+    one.backward()
+
+    class Copies(type(wl)):
+        logits = property(lambda self: np.tile(wl.logits, (copies, 1)))
+        x = property(lambda self: np.tile(wl.x, (copies, 1)))
+
+    big = make_workload("prefill", seed=212, T=1000 * copies, **kw)
+    big.__class__ = Copies
+    s = Step(big)
+    s.d_out = torch.zeros(big.T, wl.H, dtype=torch.bfloat16, device="cuda")
+    s.d_out[-1000:] = one.d_out
+    s.forward()
+    s.backward()
+    torch.cuda.synchronize()
+    # every token chose both experts: 70000 rows each
+    assert s.disp.offsets[1] == big.T and (2 * big.T - 1000) * 2 * wl.I > 2 ** 32
+    for name, v in s.b.grads.items():
+        for p in range(2):
+            ref = one.b.grads[name][p].double()
+            err = (v[p].double() - ref).norm() / ref.norm()
+            print(name, p, float(err), flush=True)
+            assert err <= 2 * B, (name, p, float(err))
 
 
 def test_two_streams_at_once():
