@@ -93,21 +93,21 @@ COUNTERS = {
     "prefill": {
         "kernel": "k_gemm_bf16<0, 4, 2, 2, 4>", "profile": "profiles/layer_gemm_bf16_prefill.md",
         "files": ["expert_moe_fp32_amd/csrc/gemm_bf16.hip", "expert_moe_fp32_amd/csrc/gemm_ring.h", "expert_moe_fp32_amd/csrc/common.h"],
-        "sha": "634d7f60892ad847",
+        "sha": "2da31bcb7492a5e0",
         "fetch_kib": 1818199.8, "fetch_factor": 1.9979,
         "write_kib": 71848.3, "write_factor": 1.0,
         "mfma_util": 0.586},
     "skewed": {
         "kernel": "k_gemm_bf16<0, 4, 2, 2, 4>", "profile": "profiles/layer_gemm_bf16_skewed.md",
         "files": ["expert_moe_fp32_amd/csrc/gemm_bf16.hip", "expert_moe_fp32_amd/csrc/gemm_ring.h", "expert_moe_fp32_amd/csrc/common.h"],
-        "sha": "634d7f60892ad847",
+        "sha": "2da31bcb7492a5e0",
         "fetch_kib": 1708994.9, "fetch_factor": 1.9979,
         "write_kib": 55172.0, "write_factor": 1.0,
         "mfma_util": 0.469},
     "skewed_eplb": {
         "kernel": "k_gemm_bf16<0, 4, 2, 2, 4>", "profile": "profiles/layer_gemm_bf16_skewed_eplb.md",
         "files": ["expert_moe_fp32_amd/csrc/gemm_bf16.hip", "expert_moe_fp32_amd/csrc/gemm_ring.h", "expert_moe_fp32_amd/csrc/common.h"],
-        "sha": "634d7f60892ad847",
+        "sha": "2da31bcb7492a5e0",
         "fetch_kib": 1991712.3, "fetch_factor": 1.9979,
         "write_kib": 55220.1, "write_factor": 1.0,
         "mfma_util": 0.421},

@@ -176,7 +176,13 @@ __global__ __launch_bounds__(kRowThreads) void k_restore_rows(
 }
 
 // Batches of fewer runs than this take one run a workgroup, so that they
-// spread over the CUs.
+// spread over the CUs; larger ones four, whose loads are in flight together.
+// One run and four, to codes and back, us: bf16, 2048 runs (1024 x 4096) 5.0 and
+// 4.9 against 5.3 and 5.0; 4096 runs 7.2 and 6.0 against 7.1 and 5.6; 5116 runs
+// (4093 x 2501, no alignment) 8.7 and 7.2 against 9.6 and 7.2; 8192 runs 11.9 and
+// 9.9 against 11.5 and 10.3; 28672 runs (8192 x 7168) 36.8 and 30.1 against 32.2
+// and 29.9.  float32, 2552 runs (1021 x 2501) 4.4 and 4.4 against 5.1 and 4.5;
+// 57344 runs (8192 x 7168) 58 and 53 against 50 and 50.
 constexpr uint32_t kManyRuns = 8192;
 
 // A launch has less than 2^32 threads (a larger grid runs only in part), so
@@ -265,9 +271,13 @@ __device__ __forceinline__ u32x2v_t checkpoint_eight(const float* v, float* scal
 
 // A wavefront's 64 lanes are 16 lanes for each of four groups of 128
 // channels, eight a lane.  Behind the rows' groups come those of the layer's
-// input (one launch of 55 us at 4096 tokens of 7168 x 2048, 32 of 256 experts
-// and the shared one, 5.2 TB/s; two launches 62, and 7.5 against 4.3 at 509
-// tokens of 1024 x 512).
+// input (one launch of 52 us at 4096 tokens of 7168 x 2048, 32 of 256 experts
+// and the shared one, 5.5 TB/s; two launches 62, and 7.5 against 4.1 at 509
+// tokens of 1024 x 512).  h is rounded to bf16, the type that the matrix cores
+// take for the down product at their full rate, as in the layer's BF16 recipe:
+// an output's error grows by it from 1.7e-3 of the output (its own rounding to
+// bf16) to 2.3e-3 in root mean square.  The codes come from the unrounded
+// products.
 __global__ __launch_bounds__(256) void k_swiglu_save(
     ExpertRows r, const float* __restrict__ gu, bf16_t* __restrict__ h,
     uint8_t* __restrict__ codes, float* __restrict__ scales,
@@ -324,7 +334,11 @@ __global__ __launch_bounds__(256) void k_swiglu_save(
 // With q = sigmoid(g):
 //   h = g q u,  dg = dh u q (1 + g (1 - q)),  du = dh g q
 // times the row's route weight w; the weight's own gradient sums dh h over
-// the row, per thread in column order, then over the threads.
+// the row, per thread in column order, then over the threads.  dg, du and w h
+// are rounded to bf16 once, for the products that follow: float32 operands would
+// run at a sixteenth of the matrix cores' bf16 rate (141 TFLOP/s against 1195 of
+// a library product), and a rounding of about 2^-9 in the mean is small beside the
+// about 2^-5 of the codes they are made from.
 __global__ __launch_bounds__(256) void k_swiglu_backward(
     ExpertRows r, PairRows pr, const float* __restrict__ dh,
     const uint8_t* __restrict__ codes, const float* __restrict__ scales,

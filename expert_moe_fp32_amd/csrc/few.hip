@@ -29,7 +29,20 @@
 //
 // FP8 weights are widened to bf16 (exactly) in registers and the product of
 // each 128-block is scaled in float32; activations stay bf16, since nothing
-// here is bound by the matrix cores.
+// here is bound by the matrix cores.  h is rounded to bf16 between the kernels,
+// for either weights: the matrix instruction's type, half the bytes that every
+// workgroup of the second kernel reads, and what the general layer's BF16 recipe
+// rounds too (an output's error grows by it from 1.7e-3 of the output, its own
+// rounding to bf16, to 2.3e-3 in root mean square).
+//
+// Against the general layer's launches, whole calls, us (32 of 256 experts, 8 a
+// token): 1, 2, 4, 8, 12 and 16 tokens of 6144 x 2048 29, 38, 60, 108-124, 154-185
+// and 184-215 against 77, 97, 103, 121-140, 160-165 and 175-180; of 7168 x 2048 in
+// FP8 with a shared expert 28, 35, 57, 89, 130 and 175 against 75, 78, 87, 97, 115
+// and 137; of 2048 x 768 15, 17, 23, 28, 34 and 39 against 39, 47, 48, 49, 49 and
+// 50; 1 token of 256 x 128, 2 of 8 experts, 9.4 against 21.  So the launches are
+// saved where few experts are in use; where some ten large ones are, their
+// weights bind and the general kernels read them faster.
 #include <type_traits>
 
 #include "few.h"

@@ -219,11 +219,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm_bf16(GArgs a) {
     // a 32-row block (8-row block r / 8, its row r % 8), chunk
     // c = 4 HH + 2 s + l / 32 at chunk slot c ^ ((r / 2) % 8); the 16 lanes
     // of a read take 16 distinct 16-byte bank groups (row parity x slot).
-    // A wavefront whose rows are all padding multiplies them too (its
-    // stores are skipped), which keeps the step one basic block.
     // Only the wavefront's first NMB row blocks hold tile rows (the rest
     // are padding of a partial tile): their fragments are read and
-    // multiplied, the others skipped.
+    // multiplied, the others skipped (NMB is a constant of each copy of the
+    // K loop, whose steps stay one basic block each).
     auto load = [&](auto nmb_c, const u32x4_t* A, int HH, const u32x4_t* B,
                     u32x4_t (&fa)[2][TM], u32x4_t (&fb)[2][TN]) {
       constexpr int NMB = decltype(nmb_c)::value;

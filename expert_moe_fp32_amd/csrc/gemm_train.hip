@@ -6,8 +6,8 @@
 // second copy of the weights is laid out.
 //
 // 4096 tokens of 7168 x 2048, 32 of 256 experts (128 rows each) and the shared
-// one: gate/up 530-570 us, down 320-350, back through down 314-330, back through
-// gate and up 640-660 (0.7 to 0.9 PFLOP/s).  Routed tiles are half full and
+// one: gate/up 535-545 us, down 320-325, back through down 355-360, back through
+// gate and up 630 (0.7 to 0.9 PFLOP/s).  Routed tiles are half full and
 // wait for their weights (2.9 GB a pass); the shared expert's tiles between them
 // fill the gaps, and an output in float32 (134 to 235 MB) is the price of an
 // activation that is checkpointed from unrounded products.
@@ -36,10 +36,10 @@ GArgs args(const TrainGemm& g, int K, int N) {
 // the latency of their stages: 64 rows x 64 columns of B (G_PAIR: 32 of gate
 // and 32 of up) from four wavefronts of 32 x 32, stages of 64 of the reduction
 // (16 KiB), four in LDS and one in registers, two workgroups a CU.  509 tokens
-// of 1024 x 512, 2 of 16 experts each: gate/up 14.2 us, down 10.1, gradients
-// back through each 13.1; stages of 128, one workgroup a CU 18.8, 11.4 and 15;
-// the ring on 256 x 256 tiles 23.7, 14.5 and 23.9, on 64 x 128 tiles (stages
-// of 32) 25.4, 15.4 and 29.
+// of 1024 x 512, 2 of 16 experts each: gate/up 13.2 us, down 9.6, back through
+// down 10.1 and through gate and up 14.8 (12.5 in the mean); stages of 128, one
+// workgroup a CU 18.8, 11.4 and 15 in the mean of the two; the ring on 256 x 256
+// tiles 23.7, 14.5 and 23.9, on 64 x 128 tiles (stages of 32) 25.4, 15.4 and 29.
 constexpr int kSmallRows = 64, kSmallColumns = 64;
 
 template <int MODE>
@@ -183,9 +183,10 @@ hipError_t launch(const TrainGemm& g, GArgs& a, int share, int chunk, hipStream_
 // weights where an expert has some hundred rows, the shared expert's for the
 // matrix cores: side by side they fill each other's gaps.  Routed tile r goes
 // to place r + floor(r S / R), shared tile j to j + ceil((j + 1) R / S), of R
-// and S of them.  Gate/up, down and d_x of 4096 tokens of 7168 x 2048, 32 of
-// 256 experts: 576, 349 and 498 us; the routed tiles first 590, 370 and 509,
-// the shared first 603, 364 and 519.
+// and S of them.  4096 tokens of 7168 x 2048, 32 of 256 experts: gate/up 536 us,
+// down 321, back through down 358, back through gate and up 630 (1845 in all);
+// the routed tiles first 546, 345, 360 and 643 (1894), the shared first 566, 344,
+// 346 and 662 (1918).
 __global__ __launch_bounds__(1024) void k_train_tiles(
     const int32_t* __restrict__ offsets, int P, int has_shared, int T, int BM,
     int4* __restrict__ tiles, int32_t* __restrict__ count) {
